@@ -66,6 +66,10 @@ typedef enum {
 #define TQ_FLAG_MAXCTX 2u    /* a sequence was longer than the decode's max_ctx: its tail was not attended */
 #define TQ_FLAG_LAYOUT 4u    /* the decode kernel found its shared memory placed other than the host
                                 checked (never expected on sm_100a): its outputs are not valid */
+#define TQ_FLAG_INDEX 8u     /* a position, slot or row given on the device was out of range or in
+                                conflict with another: see the call that took it */
+#define TQ_FLAG_TIMEOUT 16u  /* the tree attention gave up a wait inside a kernel (never expected):
+                                its outputs are not valid */
 
 typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
@@ -307,6 +311,150 @@ size_t tq_lut_matmul_workspace_bytes(const tq_codebook* cb, int rows, int k, int
 tq_status tq_lut_matmul(const tq_codebook* cb, const uint8_t* codes, const uint16_t* norms, int rows,
                         int k, const void* x, tq_dtype dtype, int m, float* y, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Speculative decoding over the compressed cache.  A step of a program that
+ * drafts several tokens and verifies them at once is
+ *   tq_rope_append    rotate q and k by their positions and append the drafts;
+ *   tq_tree_attention attend each draft to the context and its ancestors;
+ *   tq_cache_compact  keep the accepted path's slots and free the others;
+ * and tq_cache_copy forks or reorders rows (several samples of one prompt,
+ * beams).  Each call also serves without the others: a prompt's chunk is
+ * appended with rotary positions and attended as a chain, a cache is thinned
+ * by any rule that lists the kept slots.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary position embedding: pair i of a head's first rot_dim channels turns by
+ * position * f_i.  The frequencies start from f_i = base^(-2i / rot_dim).
+ *   rot_dim     : even, 2 .. 256; the channels past it are left as they are
+ *   interleaved : 0: pair i is channels (i, i + rot_dim/2); 1: (2i, 2i + 1)
+ *   scaling     : how f_i is changed for contexts longer than trained on
+ *     TQ_ROPE_NONE   f_i
+ *     TQ_ROPE_LINEAR f_i / factor
+ *     TQ_ROPE_NTK    base is replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *     TQ_ROPE_YARN   (f_i / factor) r_i + f_i (1 - r_i), r_i rising linearly from
+ *                    0 to 1 between the pairs that turn beta_fast and beta_slow
+ *                    times over original_max positions
+ *     TQ_ROPE_BANDS  (f_i / factor) (1 - s_i) + f_i s_i, s_i = clamp((turns -
+ *                    low_freq) / (high_freq - low_freq), 0, 1), turns = f_i
+ *                    original_max / 2 pi
+ *   attention_factor : multiplies cosine and sine (0: 0.1 ln(factor) + 1 for
+ *                    TQ_ROPE_YARN with factor > 1, else 1) */
+#define TQ_ROPE_NONE 0
+#define TQ_ROPE_LINEAR 1
+#define TQ_ROPE_NTK 2
+#define TQ_ROPE_YARN 3
+#define TQ_ROPE_BANDS 4
+typedef struct {
+  int rot_dim, interleaved, scaling, original_max;
+  double base, factor, beta_fast, beta_slow, low_freq, high_freq, attention_factor;
+} tq_rope_params;
+
+/* A table of rotations: DEVICE float [max_pos][rot_dim / 2][2], (cosine, sine)
+ * of every pair at every position, caller-owned, 16-byte aligned. */
+typedef struct {
+  const float *table;
+  int max_pos, rot_dim, interleaved;
+} tq_rope;
+
+/* Fills a table (max_pos >= 1).  Angles, cosines and sines are computed in
+ * float64 and rounded to float32 once, so far positions lose nothing. */
+tq_status tq_rope_table(const tq_rope_params* params, int max_pos, float* table, void* stream);
+
+/* Heads of a dense tensor: element (b, h, t, i) is data[b*stride_b + h*stride_h
+ * + t*stride_t + i] (strides in elements, the channel stride is 1).  Every
+ * stride times the element size is a multiple of 16 bytes, data is 16-byte
+ * aligned.  A slice of a fused projection [batch][T][q + k + v heads][d] and a
+ * [batch][heads][T][d] tensor are both read in place. */
+typedef struct {
+  const void *data;
+  int64_t stride_b, stride_h, stride_t;
+} tq_heads;
+
+/* tq_quantize_append with rotary positions: the keys are rotated in fp32 by the
+ * table's entries (two products and one sum per channel, each rounded) and
+ * encoded without being rounded in between; values are encoded as they are;
+ * queries, if given, are rotated and written out.
+ * q : heads of [batch][q_heads][n_new], or NULL; k, v : [batch][kv_heads][n_new]
+ * q_out : DEVICE `dtype` [batch][n_new][q_heads][head_dim] (required with q)
+ * k_out : DEVICE `dtype` [batch][n_new][kv_heads][head_dim], or NULL: the rotated
+ *         keys, for a dense attention over the same tokens
+ * positions : DEVICE int32 [batch][n_new], or NULL for start + 0, 1, 2, ...;
+ *         with relative != 0 they are added to the row's start.  A position
+ *         outside [0, max_pos) is clamped to it and sets TQ_FLAG_INDEX.
+ * start : DEVICE int32 [batch], slot of each row's first new token, or NULL for
+ *         seq_lens.  A start below seq_lens[b] discards the tokens from there
+ *         on (drafts that were refused); outside [0, seq_lens[b]] the row is
+ *         skipped and sets TQ_FLAG_INDEX.
+ * Then seq_lens[b] = start + n_new.  A row that would pass `capacity` is skipped
+ * and sets TQ_FLAG_CAPACITY.  The queries (and k_out) of a skipped row are
+ * written all the same.  Outputs must not overlap inputs.  append_sync is used
+ * as by tq_quantize_append.  n_new == 0 is a no-op. */
+tq_status tq_rope_append(const tq_codebook* cb, const tq_cache* cache, const tq_rope* rope,
+                         const tq_heads* q, int q_heads, const tq_heads* k, const tq_heads* v,
+                         tq_dtype dtype, int n_new, const int32_t* positions, int relative,
+                         const int32_t* start, void* q_out, void* k_out, void* stream);
+
+/* Workspace bytes tq_tree_attention needs for these sizes (0 on bad sizes).  It
+ * depends on the sizes alone, so one workspace serves every call (and every
+ * captured graph) of those sizes, one at a time. */
+size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, int kv_heads, int n_q,
+                               int max_ctx);
+
+/* Attention of n_q drafted tokens per batch row, whose keys and values are the
+ * row's last n_q stored tokens: draft i attends every token of the context
+ * (slots [0, seq_lens[b] - n_q)) and draft j (slot seq_lens[b] - n_q + j) if its
+ * mask says so.  Scores and values are those of tq_decode_attention.
+ * q    : DEVICE `dtype` (TQ_BF16 or TQ_F16) [batch][n_q][q_heads][head_dim], n_q 1 .. 256
+ * mask : DEVICE uint32 words, bit j % 32 of word j / 32 of row i: draft i attends
+ *        draft j; [n_q][ceil(n_q / 32)] per batch row, mask_stride words apart
+ *        (0: one mask for every row).  NULL: a chain, j <= i.
+ * out  : DEVICE `dtype`, like q.  Its operands are 16-bit: scores and weights are
+ *        accumulated in fp32, the weights and the rotated queries rounded to fp16.
+ * A draft that attends nothing gives zeros, as do all drafts of a row that holds
+ * fewer than n_q tokens.  softmax_scale, max_ctx, workspace: as for
+ * tq_decode_attention (tokens at max_ctx and past it, drafts among them, are not
+ * attended and set TQ_FLAG_MAXCTX).  q_heads / kv_heads is 1, 2, 4 or 8 and the
+ * code widths are those of the decode.  The result is deterministic. */
+tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const void* q,
+                            tq_dtype dtype, int q_heads, int n_q, const uint32_t* mask,
+                            int64_t mask_stride, float softmax_scale, int max_ctx, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keeps listed slots of every row and frees the others, in place: for i <
+ * counts[b], slot start[b] + i receives slot start[b] + index[i] of every array,
+ * and seq_lens[b] becomes start[b] + counts[b].
+ * index  : DEVICE int32, entry (b, h, i) at index[b*stride_b + h*stride_h + i];
+ *          stride_h 0: one list for all heads.  The first counts[b] entries of a
+ *          list are strictly ascending in [0, seq_lens[b] - start[b]); the others
+ *          are not read.
+ * counts : DEVICE int32 [batch], each in [0, max_count].
+ * start  : DEVICE int32 [batch] in [0, seq_lens[b]], or NULL for 0.
+ * A row whose start or count is out of range is skipped and sets TQ_FLAG_INDEX.
+ * A list that is out of range or does not ascend sets TQ_FLAG_INDEX and leaves
+ * seq_lens[b]; the row's slots from start[b] on are then unspecified.  Slots from
+ * the new length on keep what they hold or unspecified bytes of the row.
+ * append_sync is used as by tq_quantize_append. */
+tq_status tq_cache_compact(const tq_codebook* cb, const tq_cache* cache, const int32_t* index,
+                           int64_t stride_b, int64_t stride_h, const int32_t* counts, int max_count,
+                           const int32_t* start, void* stream);
+
+/* Copies rows: for i < n, row dst_rows[i] of dst receives the first len_i tokens
+ * of row src_rows[i] of src, len_i = lengths[i] (NULL: all) but at most
+ * src seq_lens, and its seq_lens becomes len_i; slots from len_i on are left as
+ * they were.  dst and src hold the same kv_heads and the same codebook's rows;
+ * they may be one cache (rows are forked).
+ * dst_rows, src_rows, lengths : DEVICE int32 [n], n at most 65535.
+ * max_len : host upper bound of every len_i (it sizes the grid); a longer one is
+ *         cut to it and sets TQ_FLAG_MAXCTX.
+ * A pair is skipped and sets TQ_FLAG_INDEX (in dst's status) when a row is out of
+ * range, when an earlier pair has the same dst row, or when dst and src are one
+ * cache and its dst row is another pair's src row; a pair of one row with itself
+ * in one cache is skipped silently.  A len_i past dst's capacity skips the pair
+ * and sets TQ_FLAG_CAPACITY; a negative length counts as 0. */
+tq_status tq_cache_copy(const tq_codebook* cb, const tq_cache* dst, const tq_cache* src,
+                        const int32_t* dst_rows, const int32_t* src_rows, const int32_t* lengths,
+                        int n, int max_len, void* stream);
 
 /* Releases a codebook (NULL is ignored). */
 void tq_free(tq_codebook* cb);

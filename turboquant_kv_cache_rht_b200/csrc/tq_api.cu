@@ -262,6 +262,55 @@ tq_status check_params(const tq_params* p) {
   return TQ_OK;
 }
 
+// Rotations per position of each pair, with the scaling for long contexts
+// applied (the formulas stand at tq_rope_params).
+tq_status rope_frequencies(const tq_rope_params& p, tq::RopeFrequencies* out) {
+  if (p.rot_dim < 2 || p.rot_dim % 2 || p.rot_dim > 256)
+    return fail(TQ_ERR_INVALID, "rot_dim %d: even, 2 .. 256", p.rot_dim);
+  if (p.scaling < TQ_ROPE_NONE || p.scaling > TQ_ROPE_BANDS)
+    return fail(TQ_ERR_INVALID, "scaling %d: one of TQ_ROPE_NONE .. TQ_ROPE_BANDS", p.scaling);
+  if (!(p.base > 1.0) || !std::isfinite(p.base)) return fail(TQ_ERR_INVALID, "base must be above 1 and finite");
+  if (p.scaling != TQ_ROPE_NONE && (!(p.factor >= 1.0) || !std::isfinite(p.factor)))
+    return fail(TQ_ERR_INVALID, "factor must be at least 1 and finite");
+  if ((p.scaling == TQ_ROPE_YARN || p.scaling == TQ_ROPE_BANDS) && p.original_max < 1)
+    return fail(TQ_ERR_INVALID, "original_max %d: at least 1", p.original_max);
+  if (p.scaling == TQ_ROPE_YARN && !(p.beta_fast > p.beta_slow && p.beta_slow > 0.0 && std::isfinite(p.beta_fast)))
+    return fail(TQ_ERR_INVALID, "beta_fast must be above beta_slow, both above 0");
+  if (p.scaling == TQ_ROPE_BANDS && !(p.high_freq > p.low_freq && p.low_freq > 0.0 && std::isfinite(p.high_freq)))
+    return fail(TQ_ERR_INVALID, "high_freq must be above low_freq, both above 0");
+  if (!(p.attention_factor >= 0.0) || !std::isfinite(p.attention_factor))
+    return fail(TQ_ERR_INVALID, "attention_factor must be finite and not negative");
+  const double rot = p.rot_dim, two_pi = 2.0 * M_PI;
+  double base = p.base;
+  if (p.scaling == TQ_ROPE_NTK && p.rot_dim > 2) base = p.base * std::pow(p.factor, rot / (rot - 2.0));
+  double low = 0.0, high = 0.0;
+  if (p.scaling == TQ_ROPE_YARN) {
+    auto pair_of = [&](double turns) {  // the pair that turns so often over original_max positions
+      return rot * std::log(p.original_max / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    low = std::fmax(std::floor(pair_of(p.beta_fast)), 0.0);
+    high = std::fmin(std::ceil(pair_of(p.beta_slow)), rot - 1.0);
+  }
+  for (int i = 0; i < p.rot_dim / 2; ++i) {
+    const double f = std::pow(base, -(2.0 * i) / rot);
+    double g = f;
+    if (p.scaling == TQ_ROPE_LINEAR) {
+      g = f / p.factor;
+    } else if (p.scaling == TQ_ROPE_YARN) {
+      const double r = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+      g = f / p.factor * r + f * (1.0 - r);
+    } else if (p.scaling == TQ_ROPE_BANDS) {
+      const double turns = p.original_max * f / two_pi;
+      const double s = std::fmin(std::fmax((turns - p.low_freq) / (p.high_freq - p.low_freq), 0.0), 1.0);
+      g = (1.0 - s) * (f / p.factor) + s * f;
+    }
+    out->freq[i] = g;
+  }
+  out->factor = p.attention_factor != 0.0 ? p.attention_factor
+                : p.scaling == TQ_ROPE_YARN && p.factor > 1.0 ? 0.1 * std::log(p.factor) + 1.0 : 1.0;
+  return TQ_OK;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 tq_status check_cache(const tq_codebook* cb, const tq_cache* c) {
@@ -309,6 +358,26 @@ tq::CacheView view_of(const tq_cache* c) {
   v.kv_heads = c->kv_heads;
   v.capacity = c->capacity;
   return v;
+}
+
+// The arrays whose slots a copy or a compaction moves, with the bytes of a slot.
+tq::SlotArrays arrays_of(const tq_codebook* cb, const tq_cache* c) {
+  const tq::Tables& t = cb->tables;
+  const int meta = t.affine ? 4 * t.d / tq::kAffineGroup : 2;
+  tq::SlotArrays a = {};
+  auto add = [&](void* p, int bytes) {
+    a.p[a.n] = static_cast<uint8_t*>(p);
+    a.bytes[a.n++] = bytes;
+  };
+  add(c->k_codes, t.k_bits * t.d / 8);
+  add(c->v_codes, t.v_bits * t.d / 8);
+  add(c->k_norm, meta);
+  add(c->v_norm, meta);
+  if (t.qjl) {
+    add(c->k_signs, t.d / 8);
+    add(c->k_rnorm, 2);
+  }
+  return a;
 }
 
 tq_status cuda_status(cudaError_t e, const char* what) {
@@ -519,6 +588,168 @@ tq_status tq_decode_attention(const tq_codebook* cb, const tq_cache* cache, cons
   return cuda_status(tq::launch_decode(cb->tables, view_of(cache), q, (int)dtype, q_heads, scale,
                                        max_ctx, out, (float*)workspace, (cudaStream_t)stream),
                      "decode launch");
+}
+
+tq_status tq_rope_table(const tq_rope_params* params, int max_pos, float* table, void* stream) {
+  if (!params) return fail(TQ_ERR_INVALID, "params is NULL");
+  if (!table) return fail(TQ_ERR_INVALID, "table is NULL");
+  if (!aligned16(table)) return fail(TQ_ERR_INVALID, "table must be 16-byte aligned");
+  if (max_pos < 1) return fail(TQ_ERR_INVALID, "max_pos %d: at least 1", max_pos);
+  tq::RopeFrequencies rf;
+  const tq_status st = rope_frequencies(*params, &rf);
+  if (st != TQ_OK) return st;
+  return cuda_status(tq::launch_rope_table(rf, params->rot_dim / 2, max_pos, table, (cudaStream_t)stream),
+                     "rope-table launch");
+}
+
+tq_status tq_rope_append(const tq_codebook* cb, const tq_cache* cache, const tq_rope* rope,
+                         const tq_heads* q, int q_heads, const tq_heads* k, const tq_heads* v,
+                         tq_dtype dtype, int n_new, const int32_t* positions, int relative,
+                         const int32_t* start, void* q_out, void* k_out, void* stream) {
+  tq_status st = check_cache(cb, cache);
+  if (st != TQ_OK) return st;
+  if (!rope || !rope->table) return fail(TQ_ERR_INVALID, "rope or its table is NULL");
+  const int d = cb->params.head_dim;
+  if (rope->rot_dim < 2 || rope->rot_dim % 2 || rope->rot_dim > d)
+    return fail(TQ_ERR_INVALID, "rot_dim %d: even, 2 .. head_dim %d", rope->rot_dim, d);
+  if (rope->max_pos < 1) return fail(TQ_ERR_INVALID, "rope max_pos %d: at least 1", rope->max_pos);
+  if (!aligned16(rope->table)) return fail(TQ_ERR_INVALID, "rope table must be 16-byte aligned");
+  if (n_new < 0) return fail(TQ_ERR_INVALID, "n_new %d is negative", n_new);
+  if (dtype != TQ_F32 && dtype != TQ_BF16 && dtype != TQ_F16)
+    return fail(TQ_ERR_INVALID, "unknown dtype %d", (int)dtype);
+  if (n_new > cache->capacity)
+    return fail(TQ_ERR_INVALID, "n_new %d exceeds capacity %d", n_new, cache->capacity);
+  if (q && q_heads <= 0) return fail(TQ_ERR_INVALID, "q_heads %d must be positive", q_heads);
+  if (n_new == 0) return ok();
+  if (!k || !v || !k->data || !v->data) return fail(TQ_ERR_INVALID, "k or v is NULL");
+  if (q && (!q->data || !q_out)) return fail(TQ_ERR_INVALID, "q needs data and q_out");
+  const tq_heads* views[] = {k, v, q};
+  const char* names[] = {"k", "v", "q"};
+  const int64_t esz = dtype == TQ_F32 ? 4 : 2;
+  for (int i = 0; i < (q ? 3 : 2); ++i) {
+    const tq_heads& h = *views[i];
+    if (h.stride_b < 0 || h.stride_h < 0 || h.stride_t < 0)
+      return fail(TQ_ERR_INVALID, "%s has a negative stride", names[i]);
+    if ((h.stride_b * esz) % 16 || (h.stride_h * esz) % 16 || (h.stride_t * esz) % 16)
+      return fail(TQ_ERR_INVALID, "strides of %s (%lld, %lld, %lld) are not multiples of 16 bytes", names[i],
+                  (long long)h.stride_b, (long long)h.stride_h, (long long)h.stride_t);
+    if (!aligned16(h.data)) return fail(TQ_ERR_INVALID, "%s must be 16-byte aligned", names[i]);
+  }
+  if (!aligned16(q_out) || !aligned16(k_out))
+    return fail(TQ_ERR_INVALID, "q_out and k_out must be 16-byte aligned");
+  if ((uintptr_t)positions % 4 || (uintptr_t)start % 4)
+    return fail(TQ_ERR_INVALID, "positions and start must be 4-byte aligned");
+  tq::RopeAppend ra;
+  ra.table = rope->table;
+  ra.max_pos = rope->max_pos;
+  ra.rot_dim = rope->rot_dim;
+  ra.interleaved = rope->interleaved != 0;
+  auto heads = [](const tq_heads* h) {
+    return h ? tq::Heads{h->data, (long)h->stride_b, (long)h->stride_h, (long)h->stride_t} : tq::Heads{};
+  };
+  ra.q = heads(q);
+  ra.k = heads(k);
+  ra.v = heads(v);
+  ra.q_out = q ? q_out : nullptr;
+  ra.k_out = k_out;
+  ra.positions = positions;
+  ra.start = start;
+  ra.relative = relative != 0;
+  ra.q_heads = q ? q_heads : 0;
+  ra.n_new = n_new;
+  return cuda_status(tq::launch_rope_append(cb->tables, view_of(cache), ra, (int)dtype, (cudaStream_t)stream),
+                     "rope-append launch");
+}
+
+tq_status tq_cache_compact(const tq_codebook* cb, const tq_cache* cache, const int32_t* index,
+                           int64_t stride_b, int64_t stride_h, const int32_t* counts, int max_count,
+                           const int32_t* start, void* stream) {
+  tq_status st = check_cache(cb, cache);
+  if (st != TQ_OK) return st;
+  if (!counts || (!index && max_count > 0)) return fail(TQ_ERR_INVALID, "index or counts is NULL");
+  if (max_count < 0 || max_count > cache->capacity)
+    return fail(TQ_ERR_INVALID, "max_count %d outside [0, capacity %d]", max_count, cache->capacity);
+  if (stride_b < 0 || stride_h < 0) return fail(TQ_ERR_INVALID, "negative stride");
+  if ((uintptr_t)index % 4 || (uintptr_t)counts % 4 || (uintptr_t)start % 4)
+    return fail(TQ_ERR_INVALID, "index, counts and start must be 4-byte aligned");
+  if (cache->kv_heads > 65535) return fail(TQ_ERR_INVALID, "kv_heads %d: at most 65535", cache->kv_heads);
+  return cuda_status(tq::launch_cache_compact(arrays_of(cb, cache), view_of(cache), index, (long)stride_b,
+                                              (long)stride_h, counts, max_count, start, (cudaStream_t)stream),
+                     "cache-compact launch");
+}
+
+tq_status tq_cache_copy(const tq_codebook* cb, const tq_cache* dst, const tq_cache* src,
+                        const int32_t* dst_rows, const int32_t* src_rows, const int32_t* lengths,
+                        int n, int max_len, void* stream) {
+  tq_status st = check_cache(cb, dst);
+  if (st != TQ_OK) return st;
+  st = check_cache(cb, src);
+  if (st != TQ_OK) return st;
+  if (dst->kv_heads != src->kv_heads)
+    return fail(TQ_ERR_INVALID, "kv_heads differ (dst %d, src %d)", dst->kv_heads, src->kv_heads);
+  if (dst->kv_heads > 65535) return fail(TQ_ERR_INVALID, "kv_heads %d: at most 65535", dst->kv_heads);
+  if (n < 0 || n > 65535) return fail(TQ_ERR_INVALID, "n %d outside [0, 65535]", n);
+  if (max_len < 0) return fail(TQ_ERR_INVALID, "max_len %d is negative", max_len);
+  if (n == 0) return ok();
+  if (!dst_rows || !src_rows) return fail(TQ_ERR_INVALID, "dst_rows or src_rows is NULL");
+  if ((uintptr_t)dst_rows % 4 || (uintptr_t)src_rows % 4 || (uintptr_t)lengths % 4)
+    return fail(TQ_ERR_INVALID, "dst_rows, src_rows and lengths must be 4-byte aligned");
+  return cuda_status(tq::launch_cache_copy(arrays_of(cb, dst), view_of(dst), arrays_of(cb, src), view_of(src),
+                                           dst_rows, src_rows, lengths, n, max_len, (cudaStream_t)stream),
+                     "cache-copy launch");
+}
+
+size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, int kv_heads, int n_q,
+                               int max_ctx) {
+  if (!cb || batch <= 0 || q_heads <= 0 || kv_heads <= 0 || max_ctx < 0 || q_heads % kv_heads != 0 ||
+      n_q < 1 || n_q > 256)
+    return 0;
+  return tq::tree_workspace_bytes(batch, q_heads, kv_heads, n_q, max_ctx, cb->params.head_dim);
+}
+
+tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const void* q,
+                            tq_dtype dtype, int q_heads, int n_q, const uint32_t* mask,
+                            int64_t mask_stride, float softmax_scale, int max_ctx, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  tq_status st = check_cache(cb, cache);
+  if (st != TQ_OK) return st;
+  if (!q || !out) return fail(TQ_ERR_INVALID, "q or out is NULL");
+  if (dtype != TQ_BF16 && dtype != TQ_F16)
+    return fail(TQ_ERR_INVALID, "dtype %d: the tree attention takes bf16 or fp16", (int)dtype);
+  if (n_q < 1 || n_q > 256) return fail(TQ_ERR_INVALID, "n_q %d outside [1, 256]", n_q);
+  if (q_heads <= 0 || q_heads % cache->kv_heads != 0)
+    return fail(TQ_ERR_INVALID, "q_heads %d is not a positive multiple of kv_heads %d", q_heads,
+                cache->kv_heads);
+  if (max_ctx < 0 || max_ctx > cache->capacity)
+    return fail(TQ_ERR_INVALID, "max_ctx %d outside [0, capacity %d]", max_ctx, cache->capacity);
+  if (!aligned16(q) || !aligned16(out)) return fail(TQ_ERR_INVALID, "q and out must be 16-byte aligned");
+  if ((uintptr_t)mask % 4) return fail(TQ_ERR_INVALID, "mask must be 4-byte aligned");
+  if (mask && mask_stride != 0 && mask_stride < (int64_t)n_q * ((n_q + 31) / 32))
+    return fail(TQ_ERR_INVALID, "mask_stride %lld is neither 0 nor a whole mask", (long long)mask_stride);
+  if (!std::isfinite(softmax_scale)) return fail(TQ_ERR_INVALID, "softmax_scale is not finite");
+  const int d = cb->params.head_dim, group = q_heads / cache->kv_heads;
+  if (!tq::decode_supported(d, group, cb->params.k_bits, cb->params.v_bits, cb->params.qjl))
+    return fail(TQ_ERR_UNSUPPORTED,
+                "no tree attention for head_dim=%d group=%d k_bits=%d v_bits=%d qjl=%d "
+                "(group must be 1, 2, 4 or 8; v_bits must be k_bits or k_bits + 1)",
+                d, group, cb->params.k_bits, cb->params.v_bits, cb->params.qjl);
+  const size_t need = tq::tree_workspace_bytes(cache->batch, q_heads, cache->kv_heads, n_q, max_ctx, d);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(TQ_ERR_CAPACITY, "workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, need);
+  if (need > 0 && !aligned16(workspace)) return fail(TQ_ERR_INVALID, "workspace must be 16-byte aligned");
+  tq::TreeArgs ta;
+  ta.q = q;
+  ta.out = out;
+  ta.mask = mask;
+  ta.mask_stride = (long)mask_stride;
+  ta.dtype = (int)dtype;
+  ta.q_heads = q_heads;
+  ta.n_q = n_q;
+  ta.max_ctx = max_ctx;
+  ta.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)d);
+  return cuda_status(tq::launch_tree(cb->tables, view_of(cache), ta, (float*)workspace, (cudaStream_t)stream),
+                     "tree-attention launch");
 }
 
 void tq_free(tq_codebook* cb) { delete cb; }

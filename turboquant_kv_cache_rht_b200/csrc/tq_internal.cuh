@@ -20,6 +20,8 @@ __device__ __forceinline__ void pdl_trigger() {
 constexpr unsigned kFlagCapacity = 1u;  // mirrors TQ_FLAG_CAPACITY
 constexpr unsigned kFlagMaxCtx = 2u;    // mirrors TQ_FLAG_MAXCTX
 constexpr unsigned kFlagLayout = 4u;    // mirrors TQ_FLAG_LAYOUT
+constexpr unsigned kFlagIndex = 8u;     // mirrors TQ_FLAG_INDEX
+constexpr unsigned kFlagTimeout = 16u;  // mirrors TQ_FLAG_TIMEOUT
 
 // Codebooks and rotation signs, passed to every kernel by value (they live in
 // the kernel parameter bank; no device allocation is needed).
@@ -109,6 +111,57 @@ cudaError_t launch_decode(const Tables& tb, const CacheView& cv, const void* q, 
                           int q_heads, float scale, int max_ctx, float* out, float* workspace,
                           cudaStream_t stream);
 bool decode_supported(int head_dim, int group, int k_bits, int v_bits, int qjl);
+
+// cos/sin of position * freq[i], times `factor`: table [max_pos][pairs][2].
+struct RopeFrequencies {
+  double freq[128];
+  double factor;
+};
+cudaError_t launch_rope_table(const RopeFrequencies& rf, int pairs, int max_pos, float* table,
+                              cudaStream_t stream);
+
+// Heads of a dense tensor (strides in elements).
+struct Heads {
+  const void* data;
+  long sb, sh, st;
+};
+struct RopeAppend {
+  const float* table;
+  int max_pos, rot_dim, interleaved;
+  Heads q, k, v;             // q.data NULL: no queries
+  void *q_out, *k_out;       // k_out NULL: the rotated keys are not written
+  const int32_t* positions;  // NULL: consecutive
+  const int32_t* start;      // NULL: seq_lens
+  int relative, q_heads, n_new;
+};
+cudaError_t launch_rope_append(const Tables& tb, const CacheView& cv, const RopeAppend& ra, int dtype,
+                               cudaStream_t stream);
+
+// The arrays of a cache whose slots are moved, with the bytes of one slot.
+struct SlotArrays {
+  uint8_t* p[6];
+  int bytes[6];
+  int n;
+};
+cudaError_t launch_cache_compact(const SlotArrays& arrays, const CacheView& cv, const int32_t* index,
+                                 long stride_b, long stride_h, const int32_t* counts, int max_count,
+                                 const int32_t* start, cudaStream_t stream);
+cudaError_t launch_cache_copy(const SlotArrays& dst_arrays, const CacheView& dst,
+                              const SlotArrays& src_arrays, const CacheView& src,
+                              const int32_t* dst_rows, const int32_t* src_rows,
+                              const int32_t* lengths, int n, int max_len, cudaStream_t stream);
+
+struct TreeArgs {
+  const void* q;
+  void* out;
+  const uint32_t* mask;  // NULL: chain
+  long mask_stride;      // words between the masks of two batch rows
+  int dtype, q_heads, n_q, max_ctx;
+  float scale;
+};
+size_t tree_workspace_bytes(int batch, int q_heads, int kv_heads, int n_q, int max_ctx, int head_dim);
+cudaError_t launch_tree(const Tables& tb, const CacheView& cv, const TreeArgs& ta, float* workspace,
+                        cudaStream_t stream);
 
 // Stores `message` as this thread's last error and returns `status`.
 int record_error(int status, const char* message);

@@ -41,39 +41,6 @@ constexpr int kAppendWarps = 8;
 // Channels per lane of the bulk layout (appends of many vectors, conversion).
 constexpr int kBulkE = 32;
 
-// The codec of one vector at its code width: Lloyd-Max (norm, codes, sketch)
-// or the affine group-64 comparison codec (scale/bias pairs in `norm`).  BITS
-// fixes the width at compile time (a grid of one kind: a third less register
-// pressure than the kernel that holds all three widths, so a third more warps
-// per SM); 0 takes it from `bits`.
-template <int D, int E, bool AFF, int BITS = 0>
-__device__ __forceinline__ void encode_vector(int bits, float (&u)[E], const Tables& tb, bool is_v,
-                                              int g, int lane, bool valid, uint8_t* codes,
-                                              uint16_t* norm, uint8_t* signs, uint16_t* rnorm,
-                                              const float* s_kcent) {
-  if constexpr (BITS != 0) {
-    if constexpr (AFF)
-      encode_affine_store<D, E, BITS>(u, tb, is_v, g, lane, valid, codes,
-                                      reinterpret_cast<uint32_t*>(norm), signs, rnorm);
-    else
-      encode_store<D, E, BITS>(u, tb, is_v, g, lane, valid, codes, norm, signs, rnorm, s_kcent);
-  } else if constexpr (AFF) {
-    uint32_t* meta = reinterpret_cast<uint32_t*>(norm);
-    if (bits == 2)
-      encode_affine_store<D, E, 2>(u, tb, is_v, g, lane, valid, codes, meta, signs, rnorm);
-    else if (bits == 3)
-      encode_affine_store<D, E, 3>(u, tb, is_v, g, lane, valid, codes, meta, signs, rnorm);
-    else
-      encode_affine_store<D, E, 4>(u, tb, is_v, g, lane, valid, codes, meta, signs, rnorm);
-  } else {
-    if (bits == 2)
-      encode_store<D, E, 2>(u, tb, is_v, g, lane, valid, codes, norm, signs, rnorm, s_kcent);
-    else if (bits == 3)
-      encode_store<D, E, 3>(u, tb, is_v, g, lane, valid, codes, norm, signs, rnorm, s_kcent);
-    else
-      encode_store<D, E, 4>(u, tb, is_v, g, lane, valid, codes, norm, signs, rnorm, s_kcent);
-  }
-}
 constexpr int kAppendThreads = 32 * kAppendWarps;
 
 // Grid: (kinds * blocks_per_kind, batch).  Blocks encode kind `first_kind`

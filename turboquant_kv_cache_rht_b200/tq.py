@@ -27,11 +27,14 @@ TQ_OK, TQ_ERR_INVALID, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_CAPACITY, TQ_ERR_
 TQ_FLAG_CAPACITY = 1
 TQ_FLAG_MAXCTX = 2
 TQ_FLAG_LAYOUT = 4
+TQ_FLAG_INDEX = 8
+TQ_FLAG_TIMEOUT = 16
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 EXPORTS = ("tq_codebook_init", "tq_codebook_tables", "tq_quantize_append", "tq_quantize_cache",
            "tq_weights_quantize", "tq_lut_matmul_workspace_bytes", "tq_lut_matmul",
            "tq_decode_workspace_bytes", "tq_decode_attention", "tq_decode_attention_noalloc",
-           "tq_free", "tq_last_error")
+           "tq_rope_table", "tq_rope_append", "tq_tree_workspace_bytes", "tq_tree_attention",
+           "tq_cache_compact", "tq_cache_copy", "tq_free", "tq_last_error")
 
 
 class tq_params(C.Structure):
@@ -53,6 +56,27 @@ class tq_cache(C.Structure):
                 ("k_norm", C.c_void_p), ("v_norm", C.c_void_p), ("k_rnorm", C.c_void_p),
                 ("seq_lens", C.c_void_p), ("status", C.c_void_p), ("append_sync", C.c_void_p),
                 ("batch", C.c_int), ("kv_heads", C.c_int), ("capacity", C.c_int)]
+
+
+class tq_rope_params(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("interleaved", C.c_int), ("scaling", C.c_int),
+                ("original_max", C.c_int), ("base", C.c_double), ("factor", C.c_double),
+                ("beta_fast", C.c_double), ("beta_slow", C.c_double), ("low_freq", C.c_double),
+                ("high_freq", C.c_double), ("attention_factor", C.c_double)]
+
+
+# TQ_ROPE_NONE, TQ_ROPE_LINEAR, TQ_ROPE_NTK, TQ_ROPE_YARN, TQ_ROPE_BANDS
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class tq_rope(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("max_pos", C.c_int), ("rot_dim", C.c_int),
+                ("interleaved", C.c_int)]
+
+
+class tq_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_int64), ("stride_h", C.c_int64),
+                ("stride_t", C.c_int64)]
 
 
 lib.tq_codebook_init.argtypes = [C.POINTER(tq_params), C.POINTER(C.c_void_p), C.POINTER(tq_layout)]
@@ -82,6 +106,24 @@ lib.tq_decode_attention.restype = C.c_int
 lib.tq_decode_attention_noalloc.argtypes = [C.c_void_p, C.POINTER(tq_cache), C.c_void_p, C.c_int,
                                             C.c_int, C.c_float, C.c_int, C.c_void_p, C.c_void_p]
 lib.tq_decode_attention_noalloc.restype = C.c_int
+lib.tq_rope_table.argtypes = [C.POINTER(tq_rope_params), C.c_int, C.c_void_p, C.c_void_p]
+lib.tq_rope_table.restype = C.c_int
+lib.tq_rope_append.argtypes = [C.c_void_p, C.POINTER(tq_cache), C.POINTER(tq_rope), C.POINTER(tq_heads),
+                               C.c_int, C.POINTER(tq_heads), C.POINTER(tq_heads), C.c_int, C.c_int,
+                               C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]
+lib.tq_rope_append.restype = C.c_int
+lib.tq_tree_workspace_bytes.argtypes = [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]
+lib.tq_tree_workspace_bytes.restype = C.c_size_t
+lib.tq_tree_attention.argtypes = [C.c_void_p, C.POINTER(tq_cache), C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                  C.c_void_p, C.c_int64, C.c_float, C.c_int, C.c_void_p, C.c_void_p,
+                                  C.c_size_t, C.c_void_p]
+lib.tq_tree_attention.restype = C.c_int
+lib.tq_cache_compact.argtypes = [C.c_void_p, C.POINTER(tq_cache), C.c_void_p, C.c_int64, C.c_int64,
+                                 C.c_void_p, C.c_int, C.c_void_p, C.c_void_p]
+lib.tq_cache_compact.restype = C.c_int
+lib.tq_cache_copy.argtypes = [C.c_void_p, C.POINTER(tq_cache), C.POINTER(tq_cache), C.c_void_p, C.c_void_p,
+                              C.c_void_p, C.c_int, C.c_int, C.c_void_p]
+lib.tq_cache_copy.restype = C.c_int
 lib.tq_free.argtypes = [C.c_void_p]
 lib.tq_free.restype = None
 lib.tq_last_error.argtypes = []
@@ -354,6 +396,236 @@ def tq_decode_attention_noalloc(cb: Codebook, cache: Cache, q: torch.Tensor,
                                            out.data_ptr(), _stream_ptr(stream)),
            "tq_decode_attention_noalloc")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Speculative decoding over the compressed cache
+# ---------------------------------------------------------------------------
+class _on:
+    """The device and stream of one call: a context in which the cache's device is
+    current and what the call allocates belongs to the stream it runs on."""
+
+    def __init__(self, device: torch.device, stream):
+        self.entered = []
+        if device.index != torch.cuda.current_device():
+            self.entered.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.entered.append(torch.cuda.stream(stream))
+
+    def __enter__(self) -> int:
+        for c in self.entered:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _index_tensor(where: str, name: str, t: torch.Tensor | None, shape) -> None:
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _check_cache(where: str, cb: Codebook, cache: Cache, device: torch.device) -> None:
+    """The arrays a call writes have the codebook's shapes and lie on the cache's device."""
+    lay, n = cb.layout, (cache.batch, cache.kv_heads, cache.capacity)
+    meta = (lay.norm_halves,) if cb.affine else ()
+    want = [("k_codes", (lay.k_code_bytes,)), ("v_codes", (lay.v_code_bytes,)), ("k_norm", meta), ("v_norm", meta)]
+    if cb.qjl:
+        want += [("k_signs", (lay.k_sign_bytes,)), ("k_rnorm", ())]
+    for name, tail in want:
+        t = getattr(cache, name)
+        if t is None or t.shape != n + tail or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor {n + tail} on {device}")
+
+
+class Rope:
+    """Rotary positions: the cosines and sines of ``max_pos`` positions for the
+    first ``rot_dim`` channels of a head (tq_rope_table), kept on the device."""
+
+    def __init__(self, rot_dim: int, max_pos: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str | None = None, factor: float = 1.0, original_max: int = 0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, low_freq: float = 1.0,
+                 high_freq: float = 4.0, attention_factor: float | None = None, device="cuda",
+                 stream=None):
+        """scaling: None, "linear", "ntk", "yarn" or "bands" (tq_rope_params gives the
+        formulas); attention_factor multiplies cosine and sine (None: 0.1 ln(factor) + 1
+        for yarn, else 1); interleaved pairs channels (2i, 2i + 1) instead of
+        (i, i + rot_dim / 2)."""
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be None or one of {sorted(k for k in ROPE_SCALINGS if k)}")
+        self.params = tq_rope_params(rot_dim, int(bool(interleaved)), ROPE_SCALINGS[scaling], original_max,
+                                     base, factor, beta_fast, beta_slow, low_freq, high_freq,
+                                     attention_factor or 0.0)
+        self.rot_dim, self.max_pos, self.interleaved = rot_dim, max_pos, bool(interleaved)
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"Rope: the table lives on a CUDA device, not on {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with _on(device, stream) as s:
+            self.table = torch.empty(max(max_pos, 1), max(rot_dim // 2, 1), 2, dtype=torch.float32, device=device)
+            _check(lib.tq_rope_table(C.byref(self.params), max_pos, self.table.data_ptr(), s), "tq_rope_table")
+
+    def struct(self) -> tq_rope:
+        return tq_rope(self.table.data_ptr(), self.max_pos, self.rot_dim, int(self.interleaved))
+
+
+def _heads(where: str, name: str, t: torch.Tensor, batch: int, heads: int | None, like: torch.Tensor) -> tq_heads:
+    if (t.dim() != 4 or t.shape[0] != batch or t.shape[2] != like.shape[2] or t.shape[3] != like.shape[3] or
+            (heads is not None and t.shape[1] != heads) or t.dtype != like.dtype):
+        raise ValueError(f"{where}: {name} must be [batch, heads, n_new, head_dim] of one dtype, matching the cache")
+    sb, sh, st, sc = t.stride()
+    if sc != 1 and t.shape[3] != 1:
+        raise ValueError(f"{where}: {name} must have a unit channel stride")
+    b, h, n, _ = t.shape   # the stride of a dimension of one is free
+    return tq_heads(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, st if n > 1 else 0)
+
+
+def tq_rope_append(cb: Codebook, cache: Cache, rope: Rope, k: torch.Tensor, v: torch.Tensor,
+                   q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                   relative: bool = False, start: torch.Tensor | None = None,
+                   keys_out: bool | torch.Tensor = False, q_out: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """tq_quantize_append with rotary positions.
+
+    k, v: [batch, kv_heads, n_new, head_dim] and q: [batch, q_heads, n_new, head_dim]
+    CUDA tensors of one dtype with unit channel stride and any other strides (views
+    of a fused projection work in place).  positions: int32 [batch, n_new] (default:
+    consecutive from the row's start); relative adds the row's start to them.
+    start: int32 [batch], the slot of each row's first new token (default: seq_lens).
+    Returns (rotated q [batch, n_new, q_heads, head_dim] or None, rotated k
+    [batch, n_new, kv_heads, head_dim] if keys_out, else None)."""
+    where, dev = "tq_rope_append", cache.seq_lens.device
+    if k.dim() != 4 or k.shape[3] != cb.head_dim:
+        raise ValueError(f"{where}: k must be [batch, kv_heads, n_new, head_dim {cb.head_dim}]")
+    hk = _heads(where, "k", k, cache.batch, cache.kv_heads, k)
+    hv = _heads(where, "v", v, cache.batch, cache.kv_heads, k)
+    hq = None if q is None else _heads(where, "q", q, cache.batch, None, k)
+    b, n, code = cache.batch, k.shape[2], _dtype_code(k)
+    _on_device(where, dev, cache=cache.seq_lens, k=k, v=v, q=q, positions=positions, start=start,
+               rope=rope.table, q_out=q_out)
+    _check_cache(where, cb, cache, dev)
+    _index_tensor(where, "positions", positions, (b, n))
+    _index_tensor(where, "start", start, (b,))
+    with _on(dev, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty(b, n, q.shape[1], cb.head_dim, dtype=k.dtype, device=dev)
+        k_out = None
+        if isinstance(keys_out, torch.Tensor):
+            k_out = keys_out
+            _on_device(where, dev, keys_out=k_out)
+        elif keys_out:
+            k_out = torch.empty(b, n, cache.kv_heads, cb.head_dim, dtype=k.dtype, device=dev)
+        for name, t, h in (("q_out", q_out, 0 if q is None else q.shape[1]), ("keys_out", k_out, cache.kv_heads)):
+            if t is not None and (t.shape != (b, n, h, cb.head_dim) or t.dtype != k.dtype or not t.is_contiguous()):
+                raise ValueError(f"{where}: {name} must be a contiguous {k.dtype} tensor {(b, n, h, cb.head_dim)}")
+        cs, rs = cache.struct(), rope.struct()
+        _check(lib.tq_rope_append(cb.handle, cs, rs, hq, 0 if q is None else q.shape[1], hk, hv, code, n,
+                                  _ptr(positions), int(bool(relative)), _ptr(start), _ptr(q_out), _ptr(k_out), s),
+               where)
+    return q_out, k_out
+
+
+def pack_tree_mask(sees: torch.Tensor) -> torch.Tensor:
+    """bool [..., n, n] (draft i attends draft j) -> the int32 words [..., n, ceil(n / 32)]
+    that tq_tree_attention takes."""
+    if sees.dtype != torch.bool or sees.dim() < 2 or sees.shape[-1] != sees.shape[-2]:
+        raise ValueError("sees must be a bool tensor [..., n, n]")
+    n = sees.shape[-1]
+    words = (n + 31) // 32
+    bits = torch.zeros(*sees.shape[:-1], 32 * words, dtype=torch.int64, device=sees.device)
+    bits[..., :n] = sees
+    w = (bits.unflatten(-1, (words, 32)) << torch.arange(32, device=sees.device)).sum(-1)
+    return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32)
+
+
+def tq_tree_workspace_bytes(cb: Codebook, batch: int, q_heads: int, kv_heads: int, n_q: int, max_ctx: int) -> int:
+    return int(lib.tq_tree_workspace_bytes(cb.handle, batch, q_heads, kv_heads, n_q, max_ctx))
+
+
+def tq_tree_attention(cb: Codebook, cache: Cache, q: torch.Tensor, mask: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, softmax_scale: float = 0.0, max_ctx: int | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the n_q tokens appended last: q [batch, n_q, q_heads, head_dim], a
+    contiguous bf16 or fp16 CUDA tensor; mask int32 [n_q, ceil(n_q / 32)] or one per
+    batch row (pack_tree_mask), None for a chain.  Returns q's shape and dtype."""
+    where, dev = "tq_tree_attention", cache.seq_lens.device
+    if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != cb.head_dim or not q.is_contiguous():
+        raise ValueError(f"{where}: q must be contiguous [batch, n_q, q_heads, head_dim]")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{where}: q must be bfloat16 or float16, not {q.dtype}")
+    b, n, hq, _ = q.shape
+    max_ctx = cache.capacity if max_ctx is None else max_ctx
+    _on_device(where, dev, cache=cache.seq_lens, q=q, mask=mask, out=out, workspace=workspace)
+    _check_cache(where, cb, cache, dev)
+    stride = 0
+    if mask is not None:
+        words = (n + 31) // 32
+        _index_tensor(where, "mask", mask, (n, words) if mask.dim() == 2 else (b, n, words))
+        stride = 0 if mask.dim() == 2 else n * words
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
+        raise ValueError(f"{where}: out must be a contiguous {q.dtype} tensor {tuple(q.shape)}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = tq_tree_workspace_bytes(cb, b, hq, cache.kv_heads, n, max_ctx)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check(lib.tq_tree_attention(cb.handle, cache.struct(), q.data_ptr(), _DTYPES[q.dtype], hq, n, _ptr(mask),
+                                     stride, float(softmax_scale), int(max_ctx), out.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), where)
+    return out
+
+
+def tq_cache_compact(cb: Codebook, cache: Cache, index: torch.Tensor, counts: torch.Tensor,
+                     start: torch.Tensor | None = None, stream=None) -> None:
+    """Keep slots start + index[b, (h,) i], i < counts[b], of every row, in order, and
+    free the others: seq_lens becomes start + counts.  index int32 [batch, n] or
+    [batch, kv_heads, n], ascending; counts int32 [batch]; start int32 [batch] (default 0)."""
+    where, dev = "tq_cache_compact", cache.seq_lens.device
+    b, h = cache.batch, cache.kv_heads
+    if index.dim() not in (2, 3):
+        raise ValueError(f"{where}: index must be [batch, n] or [batch, kv_heads, n]")
+    n = index.shape[-1]
+    _on_device(where, dev, cache=cache.seq_lens, index=index, counts=counts, start=start)
+    _check_cache(where, cb, cache, dev)
+    _index_tensor(where, "index", index, (b, n) if index.dim() == 2 else (b, h, n))
+    _index_tensor(where, "counts", counts, (b,))
+    _index_tensor(where, "start", start, (b,))
+    sb, sh = (n, 0) if index.dim() == 2 else (h * n, n)
+    with _on(dev, stream) as s:
+        _check(lib.tq_cache_compact(cb.handle, cache.struct(), index.data_ptr(), sb, sh, counts.data_ptr(), n,
+                                    _ptr(start), s), where)
+
+
+def tq_cache_copy(cb: Codebook, dst: Cache, src: Cache, dst_rows: torch.Tensor, src_rows: torch.Tensor,
+                  lengths: torch.Tensor | None = None, max_len: int | None = None, stream=None) -> None:
+    """Row dst_rows[i] of dst becomes the first lengths[i] tokens (default: all) of row
+    src_rows[i] of src; dst and src may be one cache.  Row lists and lengths are int32
+    CUDA tensors [n]; max_len bounds the lengths (default: src's capacity)."""
+    where, dev = "tq_cache_copy", dst.seq_lens.device
+    if dst_rows.dim() != 1:
+        raise ValueError(f"{where}: dst_rows must be [n]")
+    n = dst_rows.shape[0]
+    _on_device(where, dev, dst=dst.seq_lens, src=src.seq_lens, dst_rows=dst_rows, src_rows=src_rows,
+               lengths=lengths)
+    _check_cache(where, cb, dst, dev)
+    _check_cache(where, cb, src, dev)
+    for name, t in (("dst_rows", dst_rows), ("src_rows", src_rows), ("lengths", lengths)):
+        _index_tensor(where, name, t, (n,))
+    with _on(dev, stream) as s:
+        _check(lib.tq_cache_copy(cb.handle, dst.struct(), src.struct(), dst_rows.data_ptr(), src_rows.data_ptr(),
+                                 _ptr(lengths), n, src.capacity if max_len is None else int(max_len), s), where)
 
 
 def tq_free(cb: Codebook) -> None:
