@@ -704,7 +704,7 @@ size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, in
   if (!cb || batch <= 0 || q_heads <= 0 || kv_heads <= 0 || max_ctx < 0 || q_heads % kv_heads != 0 ||
       n_q < 1 || n_q > 256)
     return 0;
-  return tq::tree_workspace_bytes(batch, q_heads, kv_heads, n_q, max_ctx, cb->params.head_dim);
+  return tq::tree_workspace_bytes(cb->tables, batch, q_heads, kv_heads, n_q, max_ctx);
 }
 
 tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const void* q,
@@ -733,7 +733,7 @@ tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const 
                 "no tree attention for head_dim=%d group=%d k_bits=%d v_bits=%d qjl=%d "
                 "(group must be 1, 2, 4 or 8; v_bits must be k_bits or k_bits + 1)",
                 d, group, cb->params.k_bits, cb->params.v_bits, cb->params.qjl);
-  const size_t need = tq::tree_workspace_bytes(cache->batch, q_heads, cache->kv_heads, n_q, max_ctx, d);
+  const size_t need = tq::tree_workspace_bytes(cb->tables, cache->batch, q_heads, cache->kv_heads, n_q, max_ctx);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(TQ_ERR_CAPACITY, "workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, need);

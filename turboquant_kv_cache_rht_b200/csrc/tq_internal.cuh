@@ -159,7 +159,7 @@ struct TreeArgs {
   int dtype, q_heads, n_q, max_ctx;
   float scale;
 };
-size_t tree_workspace_bytes(int batch, int q_heads, int kv_heads, int n_q, int max_ctx, int head_dim);
+size_t tree_workspace_bytes(const Tables& tb, int batch, int q_heads, int kv_heads, int n_q, int max_ctx);
 cudaError_t launch_tree(const Tables& tb, const CacheView& cv, const TreeArgs& ta, float* workspace,
                         cudaStream_t stream);
 
