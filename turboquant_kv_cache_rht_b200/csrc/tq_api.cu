@@ -747,6 +747,7 @@ tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const 
   ta.q_heads = q_heads;
   ta.n_q = n_q;
   ta.max_ctx = max_ctx;
+  ta.log_group = group == 8 ? 3 : group == 4 ? 2 : group == 2 ? 1 : 0;
   ta.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)d);
   return cuda_status(tq::launch_tree(cb->tables, view_of(cache), ta, (float*)workspace, (cudaStream_t)stream),
                      "tree-attention launch");

@@ -157,6 +157,7 @@ struct TreeArgs {
   const uint32_t* mask;  // NULL: chain
   long mask_stride;      // words between the masks of two batch rows
   int dtype, q_heads, n_q, max_ctx;
+  int log_group;         // log2(q_heads / kv_heads)
   float scale;
 };
 size_t tree_workspace_bytes(const Tables& tb, int batch, int q_heads, int kv_heads, int n_q, int max_ctx);

@@ -24,39 +24,37 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(1000000)  // sleeps up to a millisecond; a spinning warp takes issue slots
       : "memory");
   return ok != 0;
 }
 // Waits for the phase of `parity` to complete.  Gives up after two seconds, or
 // once another wait of the block has given up (`dead`, shared memory); the
-// caller then leaves its role.
-__device__ __forceinline__ bool mbar_wait_lane(uint32_t bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try(bar, parity)) return true;
+// caller then leaves its role.  The wait proper is out of line: the roles' loops
+// have to fit the instruction caches together.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
   unsigned long long t0 = 0;
-  for (uint32_t i = 1;; ++i) {
+  for (;;) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*dead) return false;
-      unsigned long long t;
-      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-      if (t0 == 0) t0 = t;
-      else if (t - t0 > 2000000000ull) {
-        *dead = 1;
-        return false;
-      }
+    if (*dead) return false;
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > 2000000000ull) {
+      *dead = 1;
+      return false;
     }
   }
 }
-
-// The same for a whole warp, which is together again afterwards.
+__device__ __forceinline__ bool mbar_wait_lane(uint32_t bar, uint32_t parity, volatile int* dead) {
+  return mbar_try(bar, parity) || mbar_wait_long(bar, parity, dead);
+}
+// The same for a whole warp, which agrees on the answer and is together again.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-  const bool ok = mbar_wait_lane(bar, parity, dead);
-  __syncwarp();
-  return ok;
+  return __all_sync(0xffffffffu, mbar_wait_lane(bar, parity, dead));
 }
 
 // 1-D bulk copy, global to shared; both addresses and the size are multiples of 16.
@@ -130,14 +128,13 @@ __device__ __forceinline__ void ld_16x256b(uint32_t addr, float (&r)[16]) {
                  : "r"(addr + (p << 20)));
   }
 }
-__device__ __forceinline__ void wait_ld(float (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : TQ_V4(r, 0), TQ_V4(r, 4), TQ_V4(r, 8), TQ_V4(r, 12), TQ_V4(r, 16), TQ_V4(r, 20), TQ_V4(r, 24),
-                 TQ_V4(r, 28)::"memory");
-}
-__device__ __forceinline__ void wait_ld(float (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : TQ_V4(r, 0), TQ_V4(r, 4), TQ_V4(r, 8), TQ_V4(r, 12)::"memory");
+// The wait names the loaded registers (at most 30 operands may be read and
+// written by one asm), so that no use of them moves above it.
+template <int N>
+__device__ __forceinline__ void wait_ld(float (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 8) asm volatile("" : TQ_V4(r, i), TQ_V4(r, i + 4));
 }
 
 // 32 lanes x N columns: register i of a lane holds column i of its row.
@@ -170,30 +167,46 @@ __host__ __device__ constexpr uint32_t mma_idesc(int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle.  Reduction-contiguous: `stride`
-// is the distance of 8-row groups.  Row-contiguous: `lead` is the distance of
-// 64-row blocks, `stride` of groups of 8 along the reduction.
-__device__ __forceinline__ uint64_t mma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptors, 128-byte swizzle, as two words: the low one holds
+// the address (in 16-byte units, so operands advance by plain additions) and
+// `lead`, the high one `stride`.  Reduction-contiguous: `stride` is the distance
+// of 8-row groups.  Row-contiguous: `lead` is the distance of 64-row blocks,
+// `stride` of groups of 8 along the reduction.
+__host__ __device__ constexpr uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFu) | (((lead >> 4) & 0x3FFFu) << 16);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride) {
+  return ((stride >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n.reg .b64 b;\n.reg .pred p;\nsetp.ne.u32 p, %5, 0;\nmov.b64 b, {%2, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n.reg .b64 a, b;\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\nmov.b64 a, {%1, %2};\nmov.b64 b, {%3, %4};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // Arrives on `bar` when every matrix instruction issued so far has finished.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Registers of a warpgroup, out of those that the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---- others ----------------------------------------------------------------
