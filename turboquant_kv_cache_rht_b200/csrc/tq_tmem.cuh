@@ -27,30 +27,25 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(1000000)  // sleeps up to a millisecond; a spinning warp takes issue slots
+      : "r"(bar), "r"(parity), "n"(100000)  // nanoseconds to sleep: a spinning warp takes issue slots
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of `parity` to complete.  Gives up after two seconds, or
-// once another wait of the block has given up (`dead`, shared memory); the
-// caller then leaves its role.  The wait proper is out of line: the roles' loops
-// have to fit the instruction caches together.
+// Waits for the phase of `parity` to complete.  Gives up after some seconds at
+// most (40 000 tries, each of which sleeps for up to 0.1 ms), or once another
+// wait of the block has given up (`dead`, shared memory); the caller then leaves
+// its role.
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
-  unsigned long long t0 = 0;
-  for (;;) {
+#pragma unroll 1
+  for (int i = 0; i < 40000; ++i) {
     if (mbar_try(bar, parity)) return true;
     if (*dead) return false;
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    if (t0 == 0) t0 = t;
-    else if (t - t0 > 2000000000ull) {
-      *dead = 1;
-      return false;
-    }
   }
+  *dead = 1;
+  return false;
 }
 __device__ __forceinline__ bool mbar_wait_lane(uint32_t bar, uint32_t parity, volatile int* dead) {
-  return mbar_try(bar, parity) || mbar_wait_long(bar, parity, dead);
+  return __builtin_expect(mbar_try(bar, parity), 1) || mbar_wait_long(bar, parity, dead);
 }
 // The same for a whole warp, which agrees on the answer and is together again.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {

@@ -15,16 +15,16 @@
 //   warps 0-7   two softmax warpgroups.  Each takes the score columns of its own
 //               chunks (or every other tile, when one chunk holds all rows),
 //               keeps their maxima and sums and writes P to shared memory;
-//   warps 8-11  keys: a thread unpacks its token's codes through a table of code
-//               pairs into its lane of tensor memory, the product's A operand
-//               (no shared-memory round trip, no swizzle);
-//   warps 12-15 values: the same into shared memory, token rows of 64 channels;
-//   warps 16, 17 issue the matrix instructions of scores and of outputs (one
+//   warps 8-15  keys: a thread unpacks half of a token's codes through a table of
+//               code pairs into the token's lane of tensor memory, the product's A
+//               operand (no shared-memory round trip, no swizzle);
+//   warps 16-23 values: the same into shared memory, token rows of 64 channels;
+//   warps 24, 25 issue the matrix instructions of scores and of outputs (one
 //               thread's instructions would bound the kernel);
-//   warp 18     works out the block's share, announces its segments to the others
+//   warp 26     works out the block's share, announces its segments to the others
 //               and copies the packed tiles in, a few stages ahead;
-//   warp 19     copies a segment's query table in.
-// Twenty warps in seven roles share the instruction caches, and what bounds this
+//   warp 27     copies a segment's query table in.
+// Twenty-eight warps in seven roles share the instruction caches, and what bounds this
 // kernel first is fetching instructions: loops stay rolled where registers allow
 // it, and nothing that runs once per segment is unrolled.
 // A key's norm multiplies its scores, a value's norm its weights, both fp32, in
@@ -49,7 +49,7 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 128;          // tokens per tile: the matrix instruction's rows
-constexpr int kTreeThreads = 640;   // 20 warps, 96 registers each at launch
+constexpr int kTreeThreads = 896;   // 28 warps, 72 registers each at launch
 constexpr int kTreeMaxCtas = 148;   // one block per SM; the workspace is sized for it
 constexpr int kMetaSlots = 4;       // tiles whose norms are in flight
 constexpr int kMaxStages = 4;
@@ -87,21 +87,21 @@ constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarStFull = 2, kBarStEmpty = kBarS
               kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarMetaFull = kBarPEmpty + 2,
               kBarMetaEmpty = kBarMetaFull + kMetaSlots, kBarSegFull = kBarMetaEmpty + kMetaSlots,
               kBarSegEmpty = kBarSegFull + kSegs, kBarDone = kBarSegEmpty + kSegs, kBars = kBarDone + 2;
-constexpr int kSegReaders = 19;  // warps that read a segment
+constexpr int kSegReaders = 27;  // warps that read a segment
 constexpr int kMiscTmem = kBars * 8, kMiscDead = kMiscTmem + 4,
               kMiscSeg = (kMiscTmem + 8 + 31) / 32 * 32,  // [kSegs][8] ints
               kMiscM = kMiscSeg + kSegs * 32,             // running maxima [256]
-              kMiscAlpha = kMiscM + 1024,                 // rescale factors [2][64]
-              kMiscRed = kMiscAlpha + 512,                // [2][4][128]
+              kMiscAlpha = kMiscM + 1024,                 // rescale factors [4][32]
+              kMiscRed = kMiscAlpha + 512,                // [4 warpgroups][4 warps][64]
               kMiscBytes = kMiscRed + 4096;
 
 // Arrivals that complete barrier i's phase.
-__device__ __forceinline__ int bar_count(int i, bool split) {
-  if (i >= kBarStEmpty && i < kBarKFull) return 8;                                   // key and value warps
-  if ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty)) return 4;
-  if ((i >= kBarSEmpty && i < kBarPFull) || (i >= kBarPFull && i < kBarPEmpty)) return 4;
+__device__ __forceinline__ int bar_count(int i, bool split, int softmax_warps, int unpack_warps) {
+  if (i >= kBarStEmpty && i < kBarKFull) return 2 * unpack_warps;
+  if ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty)) return unpack_warps;
+  if ((i >= kBarSEmpty && i < kBarPFull) || (i >= kBarPFull && i < kBarPEmpty)) return softmax_warps / 2;
   if (i >= kBarMetaFull && i < kBarMetaEmpty) return 4;
-  if (i >= kBarMetaEmpty && i < kBarSegFull) return split ? 4 : 8;  // a tile's norms serve one warpgroup, or both
+  if (i >= kBarMetaEmpty && i < kBarSegFull) return split ? softmax_warps / 2 : softmax_warps;  // a tile's norms
   if (i >= kBarSegEmpty && i < kBarDone) return kSegReaders;
   return 1;
 }
@@ -156,23 +156,23 @@ __device__ __forceinline__ void unpack32(uint32_t row, uint32_t lut, uint32_t (&
   }
 }
 
-// f(block, pairs) for every 32 channels of a row.  The loop stays rolled: twenty
-// warps in five roles share the instruction caches, and unrolled roles starved
+// f(block, pairs) for every 32 channels of a row, or of half of it.  The loop stays rolled: the
+// roles share the instruction caches, and unrolled roles starved
 // each other (two thirds of the stalls were for instructions).
-template <int D, int BITS, typename F>
-__device__ __forceinline__ void unpack_row(uint32_t row, uint32_t lut, F f) {
+template <int N, int BITS, typename F>
+__device__ __forceinline__ void unpack_row(uint32_t row, uint32_t lut, int half, F f) {
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = half * N; c < (half + 1) * N; ++c) {
     uint32_t r[16];
     unpack32<BITS>(row + 4 * BITS * c, lut, r);
     f(c, r);
   }
 }
-template <int D, typename F>
-__device__ __forceinline__ void unpack_row(int bits, uint32_t row, uint32_t lut, F f) {
-  if (bits == 2) unpack_row<D, 2>(row, lut, f);
-  else if (bits == 3) unpack_row<D, 3>(row, lut, f);
-  else unpack_row<D, 4>(row, lut, f);
+template <int N, typename F>
+__device__ __forceinline__ void unpack_row(int bits, uint32_t row, uint32_t lut, int half, F f) {
+  if (bits == 2) unpack_row<N, 2>(row, lut, half, f);
+  else if (bits == 3) unpack_row<N, 3>(row, lut, half, f);
+  else unpack_row<N, 4>(row, lut, half, f);
 }
 
 // Fills a table with every lane's copy of every entry.
@@ -261,14 +261,14 @@ __device__ __forceinline__ bool raise_max(const Raise& a, const float (&kn)[4], 
     float q = fmaxf(up ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16));
     p = fmaxf(up2 ? q : p, __shfl_xor_sync(0xffffffffu, up2 ? p : q, 8));
     p = fmaxf(p, __shfl_xor_sync(0xffffffffu, p, 4));
-    if ((lane & 4) == 0) tm::stsf(a.sm_red + 512 * w + 4 * (16 * j2 + (up ? 8 : 0) + 2 * qd + (up2 ? 1 : 0)), p);
+    if ((lane & 4) == 0) tm::stsf(a.sm_red + 256 * w + 4 * (16 * j2 + (up ? 8 : 0) + 2 * qd + (up2 ? 1 : 0)), p);
   }
   tm::bar_sync(1 + a.wg, 128);
   if (w == 0 && lane < 8 * NJ) {
     const uint32_t at = a.a_m + 4 * lane, red = a.sm_red + 4 * lane;
     const float old = tm::ldsf(at);
-    const float mn = fmaxf(fmaxf(fmaxf(old, tm::ldsf(red)), tm::ldsf(red + 512)),
-                           fmaxf(tm::ldsf(red + 1024), tm::ldsf(red + 1536)));
+    const float mn = fmaxf(fmaxf(fmaxf(old, tm::ldsf(red)), tm::ldsf(red + 256)),
+                           fmaxf(tm::ldsf(red + 512), tm::ldsf(red + 768)));
     tm::stsf(at, mn);
     tm::stsf(a.sm_al + 4 * lane, fast_exp2(old - mn));
   }
@@ -404,8 +404,11 @@ template <int D, int CN, int CPW>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ Tables tb, const __grid_constant__ CacheView cv,
                 const __grid_constant__ TreeArgs ta, const __grid_constant__ TreePlan pl, uint8_t* __restrict__ ws) {
-  constexpr int SUB = CN < 32 ? CN : 32;   // columns a warpgroup holds at a time
-  constexpr int NSUB = CN / SUB, NJ = SUB / 8, STEPS = CPW * NSUB;
+  // Warps of the softmax, of the keys and of the values.  Wide chunks keep the
+  // softmax busiest: two warpgroups share each of theirs, 32 columns apiece.  Narrow
+  // ones wait for the codes: two warpgroups unpack each side, half a row apiece.
+  constexpr int SW = CN == 64 ? 16 : 8, KW = CN == 64 ? 4 : 8, VW = KW;
+  constexpr int SUB = CN == 64 ? 32 : CN, NJ = SUB / 8;  // columns of a warpgroup
   constexpr int MB = D == 256 ? 2 : 1;     // 128-channel blocks of the output
   constexpr int NG = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -424,9 +427,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
   for (int i = 0; i < (pl.lut_v != pl.lut_k ? 2 : 1); ++i)
     fill_lut(i ? pl.lut_v : pl.lut_k, i ? tb.v_bits : tb.k_bits, i ? tb.v_cent : tb.k_cent, i ? tb.v_lam : tb.k_lam);
-  if (tid < kBars) tm::mbar_init(bar(tid), bar_count(tid, split));
+  if (tid < kBars) tm::mbar_init(bar(tid), bar_count(tid, split, SW, KW));
   if (tid == 0) *dead = 0;
-  if (warp == 16) tm::alloc_all(misc + kMiscTmem);
+  if (warp == 24) tm::alloc_all(misc + kMiscTmem);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   tm::fence_before();
   __syncthreads();
@@ -438,19 +441,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint32_t seg_n = 0;
   bool fail = false;
 
-  // Registers move to the softmax: 2 x 136 + 80 + 80 + 48 = 5 x 96.
-  if (warp < 8) {
-    tm::regs_up<136>();
+  // Registers move to the softmax: 4 x 88 + 56 + 56 + 40 = 7 x 72, or
+  // 2 x 128 + 5 x 48 = 496 of these 504.
+  if (warp < SW) {
+    tm::regs_up<CN == 64 ? 88 : 128>();
     // =========================== softmax ===================================
     const int wg = warp >> 2, w = warp & 3, g = lane >> 2, qd = lane & 3;
+    // the score and weight buffers of this warpgroup, and its first column in them
+    const int buf = CN == 64 ? wg >> 1 : wg, part = CN == 64 ? 32 * (wg & 1) : 0;
     const uint32_t lanes = (uint32_t)(32 * w) << 16;
-    const uint32_t t_s = tmem + pl.tm_s + wg * CN + lanes, sm_p = pl.sm_p + wg * (CN == 64 ? 16384 : 0);
-    const uint32_t sm_m = misc + kMiscM, sm_al = misc + kMiscAlpha + wg * 256, sm_red = misc + kMiscRed + wg * 2048;
+    const uint32_t t_s = tmem + pl.tm_s + buf * CN + part + lanes, sm_p = pl.sm_p + buf * (CN == 64 ? 16384 : 0);
+    const uint32_t sm_m = misc + kMiscM, sm_al = misc + kMiscAlpha + wg * 128, sm_red = misc + kMiscRed + wg * 1024;
     // scores: folds softmax scale, log2(e) and the 1/sqrt(d) of the rotation (and of the dequantization)
     const float post0 = ta.scale * 1.4426950408889634f / (tb.affine ? sqrtf((float)D) : (float)D * tb.k_lam);
     const int live_rows = ta.n_q << ta.log_group, words = (ta.n_q + 31) >> 5;
-    const int stride = split ? 2 : 1, first = split ? wg : 0, units = cv.kv_heads * pl.blocks;
-    float l[STEPS][2 * NJ];             // this thread's part of the sums
+    const int stride = split ? 2 : 1, first = split ? buf : 0, units = cv.kv_heads * pl.blocks;
+    float l[CPW][2 * NJ];               // this thread's part of the sums; the current chunk's first
     uint32_t n_items = 0, n_tiles = 0;  // chunks done, tiles of all segments before this one
     pdl_wait();
     while (true) {
@@ -462,10 +468,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const float post = post0 / reinterpret_cast<const float*>(ws + pl.ws_scale)[unit];
       const int ctx = min(max(cv.seq_lens[sg.b], 0), cv.capacity) - ta.n_q;
       const uint32_t* mask = ta.mask ? ta.mask + sg.b * ta.mask_stride : nullptr;
-      for (int i = tid & 127; i < CN * CPW; i += 128)
-        tm::stsf(sm_m + 4 * (split ? wg * CN + i : (2 * (i / CN) + wg) * CN + i % CN), kNoMax);
-#pragma unroll 1
-      for (int s = 0; s < STEPS; ++s)
+      // column of the outputs (and maxima) of column i of this warpgroup's
+      auto column = [&](int i) { return (split ? buf : 2 * (i / SUB) + buf) * CN + part + i % SUB; };
+      if ((tid & 127) < SUB * CPW) tm::stsf(sm_m + 4 * column(tid & 127), kNoMax);
+#pragma unroll
+      for (int s = 0; s < CPW; ++s)
 #pragma unroll
         for (int j = 0; j < 2 * NJ; ++j) l[s][j] = 0.f;
       tm::bar_sync(1 + wg, 128);
@@ -487,22 +494,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
         if (lane == 0) tm::mbar_arrive(bar(kBarMetaEmpty + slot));
 #pragma unroll 1
-        for (int step = 0; step < STEPS; ++step) {  // this warpgroup's chunks, SUB columns at a time
-          const int sub = NSUB == 1 ? 0 : step & (NSUB - 1), chunk = split ? 0 : 2 * (step / NSUB) + wg;
-          const int col0 = (split ? wg : chunk) * CN + sub * SUB;  // of O and of the maxima
-          if (sub == 0) {
-            fail = !tm::mbar_wait(bar(kBarSFull + wg), n_items & 1, dead) || fail;
-            tm::fence_after();
-          }
+        for (int step = 0; step < CPW; ++step) {  // this warpgroup's chunks
+          const int chunk = split ? 0 : 2 * step + buf;
+          const int col0 = (split ? buf : chunk) * CN + part;  // of the outputs and of the maxima
+          fail = !tm::mbar_wait(bar(kBarSFull + buf), n_items & 1, dead) || fail;
+          tm::fence_after();
           float y[8 * NJ];
           uint32_t vis = 0xffffffffu;
-          if (masked)
-            vis = visible<NJ>(tok0, sg.len, ctx, row0 + chunk * CN + sub * SUB + 2 * qd, live_rows, ta.log_group, mask,
+          if (__builtin_expect(masked, 0))
+            vis = visible<NJ>(tok0, sg.len, ctx, row0 + chunk * CN + part + 2 * qd, live_rows, ta.log_group, mask,
                               words);
           bool again = false;
           while (true) {
             float2 m2[NJ];
-            tm::ld_16x256b(t_s + sub * SUB, y);
+            tm::ld_16x256b(t_s, y);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
               const uint2 x = tm::lds64(sm_m + 4 * (col0 + 8 * j + 2 * qd));
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 y[i] = x.x;
                 y[i + 1] = x.y;
               }
-            if (masked) {
+            if (__builtin_expect(masked, 0)) {
 #pragma unroll
               for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -540,31 +545,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // below 2^14 whatever the norms) moves only when a score passes it by that:
             // after the first tiles almost never, and all four warps vote together.
             again = tm::bar_or(1 + wg, 128, top > kTreeLazyLog2);
-            if (!again) break;
-            const Raise r{t_s + sub * SUB, tmem + lanes + col0, sm_m + 4 * col0, sm_al, sm_red,
-                          (uint32_t)bar(kBarPEmpty + wg), vis, (n_items & 1) ^ 1, wg, pl.cols,
+            if (__builtin_expect(!again, 1)) break;
+            const Raise r{t_s, tmem + lanes + col0, sm_m + 4 * col0, sm_al, sm_red,
+                          (uint32_t)bar(kBarPEmpty + buf), vis, (n_items & 1) ^ 1, wg, pl.cols,
                           it > first && (D > 64 || w < 2) ? MB : 0};
             fail = !raise_max<NJ>(r, kn, ev, dead) || fail;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
               const uint2 x = tm::lds64(sm_al + 4 * (8 * j + 2 * qd));
-              l[step][2 * j] *= __uint_as_float(x.x);
-              l[step][2 * j + 1] *= __uint_as_float(x.y);
+              l[0][2 * j] *= __uint_as_float(x.x);
+              l[0][2 * j + 1] *= __uint_as_float(x.y);
             }
           }
-          if (sub == NSUB - 1) {  // the scores are in registers: the next chunk's may come
-            tm::fence_before();
-            __syncwarp();
-            if (lane == 0) tm::mbar_arrive(bar(kBarSEmpty + wg));
-          }
-          if (sub == 0) fail = !tm::mbar_wait(bar(kBarPEmpty + wg), (n_items & 1) ^ 1, dead) || fail;
-          float lr[2 * NJ];  // (l lives in local memory when there are several steps)
-#pragma unroll
-          for (int j = 0; j < 2 * NJ; ++j) lr[j] = l[step][j];
+          // the scores are in registers: the next chunk's may come
+          tm::fence_before();
+          __syncwarp();
+          if (lane == 0) tm::mbar_arrive(bar(kBarSEmpty + buf));
+          fail = !tm::mbar_wait(bar(kBarPEmpty + buf), (n_items & 1) ^ 1, dead) || fail;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             uint32_t pk[4];
-            float2 sum = make_float2(lr[2 * j], lr[2 * j + 1]);
+            float2 sum = make_float2(l[0][2 * j], l[0][2 * j + 1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int i = y_at<NJ>(k, j);
@@ -574,51 +575,55 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const __half2 hw = __floats2half2_rn(wt.x, wt.y);
               pk[k] = *reinterpret_cast<const uint32_t*>(&hw);
             }
-            lr[2 * j] = sum.x;
-            lr[2 * j + 1] = sum.y;
-            tm::stmatrix_x4(sm_p + (32 * w + lane) * 128 + (((sub * NJ + j + (CN == 64 ? 0 : 4 * wg)) ^ (lane & 7)) << 4),
+            l[0][2 * j] = sum.x;
+            l[0][2 * j + 1] = sum.y;
+            tm::stmatrix_x4(sm_p + (32 * w + lane) * 128 + (((j + (CN == 64 ? part / 8 : 4 * wg)) ^ (lane & 7)) << 4),
                             pk[0], pk[1], pk[2], pk[3]);
           }
+          tm::fence_proxy_async();
+          tm::fence_before();
+          __syncwarp();
+          if (lane == 0) tm::mbar_arrive(bar(kBarPFull + buf));
+          ++n_items;
+          if constexpr (CPW == 2) {  // the other chunk's sums come to the front (registers have no index)
 #pragma unroll
-          for (int j = 0; j < 2 * NJ; ++j) l[step][j] = lr[j];
-          if (sub == NSUB - 1) {
-            tm::fence_proxy_async();
-            tm::fence_before();
-            __syncwarp();
-            if (lane == 0) tm::mbar_arrive(bar(kBarPFull + wg));
-            ++n_items;
+            for (int j = 0; j < 2 * NJ; ++j) {
+              const float x = l[0][j];
+              l[0][j] = l[1][j];
+              l[1][j] = x;
+            }
           }
         }
       }
       n_tiles += sg.tiles;
       // ---- the unit's partial
-      fail = !tm::mbar_wait(bar(kBarPEmpty + wg), (n_items & 1) ^ 1, dead) || fail;
+      fail = !tm::mbar_wait(bar(kBarPEmpty + buf), (n_items & 1) ^ 1, dead) || fail;
       tm::fence_after();
       const bool any = first < sg.tiles;
       const long pcol = (blockIdx.x + unit) * pl.cols;  // first column of the partial
-#pragma unroll 1
-      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int s = 0; s < CPW; ++s)
 #pragma unroll
         for (int j = 0; j < 2 * NJ; ++j) {
           float x = l[s][j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (g == 0) tm::stsf(sm_red + 512 * w + 4 * (s * SUB + 8 * (j >> 1) + 2 * qd + (j & 1)), x);
+          if (g == 0) tm::stsf(sm_red + 256 * w + 4 * (s * SUB + 8 * (j >> 1) + 2 * qd + (j & 1)), x);
         }
       tm::bar_sync(1 + wg, 128);
-      for (int i = tid & 127; i < CN * CPW; i += 128) {
-        const int col = split ? wg * CN + i : (2 * (i / CN) + wg) * CN + i % CN;
-        const float x = (tm::ldsf(sm_red + 4 * i) + tm::ldsf(sm_red + 512 + 4 * i)) +
-                        (tm::ldsf(sm_red + 1024 + 4 * i) + tm::ldsf(sm_red + 1536 + 4 * i));
-        reinterpret_cast<float2*>(ws + pl.ws_ml)[pcol + col] = make_float2(tm::ldsf(sm_m + 4 * col), any ? x : 0.f);
+      const int i0 = tid & 127;
+      if (i0 < SUB * CPW) {
+        const float x = (tm::ldsf(sm_red + 4 * i0) + tm::ldsf(sm_red + 256 + 4 * i0)) +
+                        (tm::ldsf(sm_red + 512 + 4 * i0) + tm::ldsf(sm_red + 768 + 4 * i0));
+        reinterpret_cast<float2*>(ws + pl.ws_ml)[pcol + column(i0)] =
+            make_float2(tm::ldsf(sm_m + 4 * column(i0)), any ? x : 0.f);
       }
       if (any && (D > 64 || w < 2)) {
         float* wo = reinterpret_cast<float*>(ws) + pcol * D + 32 * w + lane;
 #pragma unroll 1
-        for (int i = 0; i < MB * CPW * (CN / 16); ++i) {  // 16 columns at a time
-          const int h = i % (CN / 16), c = i / (CN / 16) % CPW, mb = i / (CN / 16) / CPW;
-          const int chunk = split ? 0 : 2 * c + wg, col = (split ? wg : chunk) * CN + 16 * h;
-          if (row0 + chunk * CN + 16 * h >= live_rows) continue;  // (columns without rows)
+        for (int i = 0; i < MB * CPW * (SUB / 16); ++i) {  // 16 columns at a time
+          const int mb = i / (CPW * (SUB / 16)), c = 16 * (i % (CPW * (SUB / 16))), col = column(c);
+          if (row0 + (split ? col - buf * CN : col) >= live_rows) continue;  // (columns without rows)
           uint32_t o[16];
           tm::ld_32x32b(tmem + lanes + mb * pl.cols + col, o);
           tm::wait_ld(o);
@@ -628,10 +633,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       tm::fence_before();
     }
-  } else if (warp < 12) {
-    tm::regs_down<80>();
+  } else if (warp < SW + KW) {
+    tm::regs_down<CN == 64 ? 56 : 48>();
     // =========================== keys ======================================
-    const int w = warp & 3, tok = 32 * w + lane, row_bytes = tb.k_bits * D / 8;
+    const int w = warp & 3, half = KW == 8 ? (warp >> 2) & 1 : 0, tok = 32 * w + lane, row_bytes = tb.k_bits * D / 8;
     const uint32_t lut = pl.lut_k | (tb.k_bits == 3 ? lane * 4 : tb.k_bits == 2 ? (lane & 15) * 8 : (lane & 15) * 4);
     const float sketch = tb.affine ? sqrtf(3.14159265358979f / (2.0f * D)) : sqrtf(3.14159265358979f / 2.0f) * tb.k_lam;
     uint32_t n = 0;  // tiles done
@@ -682,16 +687,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           vn = 0.f;
           kn = __int_as_float(0x7fffffff);
         }
-        const uint32_t a_meta = pl.sm_meta + slot * 1536 + 4 * tok;
-        tm::stsf(a_meta, kn);
-        tm::stsf(a_meta + 512, vn);
-        tm::stsf(a_meta + 1024, ev);
-        __syncwarp();
-        if (lane == 0) tm::mbar_arrive(bar(kBarMetaFull + slot));
+        if (half == 0) {
+          const uint32_t a_meta = pl.sm_meta + slot * 1536 + 4 * tok;
+          tm::stsf(a_meta, kn);
+          tm::stsf(a_meta + 512, vn);
+          tm::stsf(a_meta + 1024, ev);
+          __syncwarp();
+          if (lane == 0) tm::mbar_arrive(bar(kBarMetaFull + slot));
+        }
         // ---- channels, then signs
         tm::fence_after();
         const uint32_t dst = tmem + pl.tm_k + kb * pl.kcols + ((uint32_t)(32 * w) << 16);
-        unpack_row<D>(tb.k_bits, stage + tok * row_bytes, lut, [&](int c, uint32_t (&r)[16]) {
+        unpack_row<D / 8 / KW>(tb.k_bits, stage + tok * row_bytes, lut, half, [&](int c, uint32_t (&r)[16]) {
           if (tb.affine) {
             const uint32_t x = tm::lds32(stage + pl.st_kn + (tok * NG + (c >> 1)) * 4);
             const uint32_t s = __byte_perm(x, x, 0x1010), b = __byte_perm(x, x, 0x3232);
@@ -703,7 +710,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (tb.qjl) {
           const uint32_t rr = pack_half2(__float2half_rn(ratio), __float2half_rn(ratio));
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = half * (D / 8 / KW); c < (half + 1) * (D / 8 / KW); ++c) {
             const uint32_t x = ~tm::lds32(stage + pl.st_s + tok * (D / 8) + 4 * c);  // bit 1: +
             uint32_t r[16];
 #pragma unroll
@@ -722,10 +729,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (++kb == pl.nkb) kb = 0, k_ph ^= 1;
       }
     }
-  } else if (warp < 16) {
-    tm::regs_down<80>();
+  } else if (warp < SW + KW + VW) {
+    tm::regs_down<CN == 64 ? 56 : 48>();
     // =========================== values ====================================
-    const int w = warp & 3, tok = 32 * w + lane, row_bytes = tb.v_bits * D / 8;
+    const int w = warp & 3, half = KW == 8 ? (warp >> 2) & 1 : 0, tok = 32 * w + lane, row_bytes = tb.v_bits * D / 8;
     const uint32_t lut = pl.lut_v | (tb.v_bits == 3 ? lane * 4 : tb.v_bits == 2 ? (lane & 15) * 8 : (lane & 15) * 4);
     int st = 0, st_ph = 0, vb = 0, v_ph = 0;
     while (next_segment(misc, seg_n, sg, fail, dead)) {
@@ -750,7 +757,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           mul |= mul << 16;
         }
         const uint32_t dst = pl.sm_v + vb * (kTile * D * 2) + tok * 128;
-        unpack_row<D>(tb.v_bits, stage + pl.st_v + tok * row_bytes, lut, [&](int c, uint32_t (&r)[16]) {
+        unpack_row<D / 8 / VW>(tb.v_bits, stage + pl.st_v + tok * row_bytes, lut, half, [&](int c, uint32_t (&r)[16]) {
           if (tb.affine) {
             const uint32_t x = hmul2_bits(tm::lds32(stage + pl.st_vn + (tok * NG + (c >> 1)) * 4), mul);
             const uint32_t s = __byte_perm(x, x, 0x1010), b = __byte_perm(x, x, 0x3232);
@@ -773,9 +780,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
     }
   } else {
-    tm::regs_down<48>();
+    tm::regs_down<CN == 64 ? 40 : 48>();
     const uint32_t d_hi = tm::desc_hi(1024);
-    if (warp == 16) {
+    if (warp == 24) {
       // ========================= scores ======================================
       const uint32_t id = tm::mma_idesc(CN, false, false), d_q = tm::desc_lo(pl.sm_q, 16);
       const uint32_t q_blk = pl.rows * 128 / 16, q_part = pl.rows * D * 2 / 16;
@@ -817,7 +824,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (++kb == (uint32_t)pl.nkb) kb = 0, k_ph ^= 1;
         }
       }
-    } else if (warp == 17) {
+    } else if (warp == 25) {
       // ========================= outputs =====================================
       const uint32_t id = tm::mma_idesc(CN, true, true), d_v = tm::desc_lo(pl.sm_v, D == 64 ? 0 : 16384),
                      d_p = tm::desc_lo(pl.sm_p, 16);
@@ -852,7 +859,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (++vb == (uint32_t)pl.nvb) vb = 0, v_ph ^= 1;
         }
       }
-    } else if (warp == 18) {
+    } else if (warp == 26) {
       // ========================= share, segments, packed tiles ===============
       // This block takes tiles [t, t1) of the T laid end to end over all units.
       const int n_q = ta.n_q, max_ctx = ta.max_ctx, units = cv.kv_heads * pl.blocks;
@@ -961,17 +968,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       __syncwarp();
     }
-    if (warp < 18 && fail && lane == 0) {  // after a failure the products in flight are waited for
+    if (warp < 26 && fail && lane == 0) {  // after a failure the products in flight are waited for
       int never = 0;
-      tm::mma_commit(bar(kBarDone + warp - 16));
-      tm::mbar_wait_lane(bar(kBarDone + warp - 16), 0, &never);
+      tm::mma_commit(bar(kBarDone + warp - 24));
+      tm::mbar_wait_lane(bar(kBarDone + warp - 24), 0, &never);
     }
     __syncwarp();
   }
   tm::fence_before();
   __syncthreads();
   if (tid == 0 && *dead) atomicOr(cv.status, (int)kFlagTimeout);
-  if (warp == 16) {
+  if (warp == 24) {
     tm::fence_after();
     tm::dealloc_all(tmem);
   }
