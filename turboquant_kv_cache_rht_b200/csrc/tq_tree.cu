@@ -128,7 +128,7 @@ __device__ __forceinline__ bool next_segment(uint32_t misc, uint32_t& n, Segment
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tm::mbar_arrive(misc + 8 * (kBarSegEmpty + slot));
   ++n;
-  return s.tiles > 0 && !__any_sync(0xffffffffu, fail);
+  return __all_sync(0xffffffffu, s.tiles > 0 && !fail);
 }
 
 // 32 channels of a packed row at shared address `row` -> 16 fp16 pairs.
@@ -434,7 +434,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tm::fence_before();
   __syncthreads();
   tm::fence_after();
-  const uint32_t tmem = tm::lds32(misc + kMiscTmem);
+  // all of the tensor memory is this block's, so it starts at address 0: a constant,
+  // which the matrix instructions (operands in uniform registers) are issued fastest from
+  constexpr uint32_t tmem = 0;
+  if (tm::lds32(misc + kMiscTmem) != tmem) {
+    if (tid == 0) atomicOr(cv.status, (int)kFlagLayout);
+    if (warp == 24) tm::dealloc_all(tm::lds32(misc + kMiscTmem));
+    return;
+  }
   pdl_trigger();
 
   Segment sg;
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         fail = !tm::mbar_wait(bar(kBarQFull), (seg_n - 1) & 1, dead);
         buf = 0;
 #pragma unroll 1
-        for (int t = 0; t < sg.tiles && !fail; ++t) {
+        for (int t = 0; !fail && __any_sync(0xffffffffu, t < sg.tiles); ++t) {  // (votes: uniform to the compiler too)
           fail = !tm::mbar_wait(bar(kBarKFull + kb), k_ph, dead);
           const uint32_t a = tmem + pl.tm_k + kb * pl.kcols;
           uint32_t bq = d_q;
@@ -832,7 +839,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       while (next_segment(misc, seg_n, sg, fail, dead)) {
         buf = 0;
 #pragma unroll 1
-        for (int t = 0; t < sg.tiles && !fail; ++t) {
+        for (int t = 0; !fail && __any_sync(0xffffffffu, t < sg.tiles); ++t) {
           fail = !tm::mbar_wait(bar(kBarVFull + vb), v_ph, dead);
           const uint32_t acc = split ? t >= 2 : t >= 1;  // the first of a unit's products overwrites
           uint32_t d = tmem + (split ? buf * CN : 0);

@@ -403,9 +403,15 @@ def tq_decode_attention_noalloc(cb: Codebook, cache: Cache, q: torch.Tensor,
 # ---------------------------------------------------------------------------
 class _on:
     """The device and stream of one call: a context in which the cache's device is
-    current and what the call allocates belongs to the stream it runs on."""
+    current and what the call allocates belongs to the stream it runs on; it gives
+    the stream's address.  Nothing is switched where both are current already."""
+
+    __slots__ = ("entered", "index")
 
     def __init__(self, device: torch.device, stream):
+        self.entered, self.index = (), device.index
+        if stream is None and device.index == torch.cuda.current_device():
+            return
         self.entered = []
         if device.index != torch.cuda.current_device():
             self.entered.append(torch.cuda.device(device))
@@ -417,7 +423,7 @@ class _on:
     def __enter__(self) -> int:
         for c in self.entered:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.entered):
@@ -428,22 +434,40 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _index_tensor(where: str, name: str, t: torch.Tensor | None, shape) -> None:
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+def _refuse_device(where: str, name: str, t: torch.Tensor, device: torch.device):
+    raise ValueError(f"{where}: {name} must be a CUDA tensor on {device}, not on {t.device}")
+
+
+def _index_ptr(where: str, name: str, t: torch.Tensor | None, shape: tuple, device: torch.device):
+    """The address of an int32 argument of this shape, None for none."""
+    if t is None:
+        return None
+    if t.device != device:
+        _refuse_device(where, name, t, device)
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
 
 
-def _check_cache(where: str, cb: Codebook, cache: Cache, device: torch.device) -> None:
-    """The arrays a call writes have the codebook's shapes and lie on the cache's device."""
+def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) -> tq_cache:
+    """The cache's arrays, which have the codebook's shapes and lie on its device."""
+    if device.type != "cuda":
+        _refuse_device(where, "cache", cache.seq_lens, device)
     lay, n = cb.layout, (cache.batch, cache.kv_heads, cache.capacity)
-    meta = (lay.norm_halves,) if cb.affine else ()
-    want = [("k_codes", (lay.k_code_bytes,)), ("v_codes", (lay.v_code_bytes,)), ("k_norm", meta), ("v_norm", meta)]
+    meta = n + (lay.norm_halves,) if cb.affine else n
+    kc, vc, kn, vn = cache.k_codes, cache.v_codes, cache.k_norm, cache.v_norm
+    ks, kr = (cache.k_signs, cache.k_rnorm) if cb.qjl else (None, None)
+    sl, st, sy = cache.seq_lens, cache.status, cache.append_sync
+    want = ((kc, n + (lay.k_code_bytes,)), (vc, n + (lay.v_code_bytes,)), (kn, meta), (vn, meta),
+            (sl, n[:1]), (st, (1,)), (sy, n[:1]))
     if cb.qjl:
-        want += [("k_signs", (lay.k_sign_bytes,)), ("k_rnorm", ())]
-    for name, tail in want:
-        t = getattr(cache, name)
-        if t is None or t.shape != n + tail or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor {n + tail} on {device}")
+        want += ((ks, n + (lay.k_sign_bytes,)), (kr, n))
+    for t, shape in want:
+        if t is None or t.shape != shape or t.device != device or not t.is_contiguous():
+            name = next(k for k, v in vars(cache).items() if v is t)
+            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor {shape} on {device}")
+    return tq_cache(kc.data_ptr(), vc.data_ptr(), _ptr(ks), kn.data_ptr(), vn.data_ptr(), _ptr(kr), sl.data_ptr(),
+                    st.data_ptr(), sy.data_ptr(), *n)
 
 
 class Rope:
@@ -478,14 +502,16 @@ class Rope:
         return tq_rope(self.table.data_ptr(), self.max_pos, self.rot_dim, int(self.interleaved))
 
 
-def _heads(where: str, name: str, t: torch.Tensor, batch: int, heads: int | None, like: torch.Tensor) -> tq_heads:
-    if (t.dim() != 4 or t.shape[0] != batch or t.shape[2] != like.shape[2] or t.shape[3] != like.shape[3] or
-            (heads is not None and t.shape[1] != heads) or t.dtype != like.dtype):
+def _heads(where: str, name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype,
+           device: torch.device) -> tq_heads:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{where}: {name} must be [batch, heads, n_new, head_dim] of one dtype, matching the cache")
+    if t.device != device:
+        _refuse_device(where, name, t, device)
     sb, sh, st, sc = t.stride()
-    if sc != 1 and t.shape[3] != 1:
+    if sc != 1:
         raise ValueError(f"{where}: {name} must have a unit channel stride")
-    b, h, n, _ = t.shape   # the stride of a dimension of one is free
+    b, h, n, _ = shape   # the stride of a dimension of one is free
     return tq_heads(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, st if n > 1 else 0)
 
 
@@ -506,32 +532,43 @@ def tq_rope_append(cb: Codebook, cache: Cache, rope: Rope, k: torch.Tensor, v: t
     where, dev = "tq_rope_append", cache.seq_lens.device
     if k.dim() != 4 or k.shape[3] != cb.head_dim:
         raise ValueError(f"{where}: k must be [batch, kv_heads, n_new, head_dim {cb.head_dim}]")
-    hk = _heads(where, "k", k, cache.batch, cache.kv_heads, k)
-    hv = _heads(where, "v", v, cache.batch, cache.kv_heads, k)
-    hq = None if q is None else _heads(where, "q", q, cache.batch, None, k)
-    b, n, code = cache.batch, k.shape[2], _dtype_code(k)
-    _on_device(where, dev, cache=cache.seq_lens, k=k, v=v, q=q, positions=positions, start=start,
-               rope=rope.table, q_out=q_out)
-    _check_cache(where, cb, cache, dev)
-    _index_tensor(where, "positions", positions, (b, n))
-    _index_tensor(where, "start", start, (b,))
+    b, hk, n, d = shape = (cache.batch, cache.kv_heads, k.shape[2], cb.head_dim)
+    dtype, hq = k.dtype, 0
+    code = _dtype_code(k)
+    kv = _heads(where, "k", k, shape, dtype, dev)
+    vv = _heads(where, "v", v, shape, dtype, dev)
+    qv = None
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 4 else 0
+        qv = _heads(where, "q", q, (b, hq, n, d), dtype, dev)
+    if rope.table.device != dev:
+        _refuse_device(where, "rope", rope.table, dev)
+    pos = _index_ptr(where, "positions", positions, (b, n), dev)
+    begin = _index_ptr(where, "start", start, (b,), dev)
+    cs = _cache_struct(where, cb, cache, dev)
     with _on(dev, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty(b, n, q.shape[1], cb.head_dim, dtype=k.dtype, device=dev)
+        if q is None:
+            q_out = None
+        elif q_out is None:
+            q_out = torch.empty((b, n, hq, d), dtype=dtype, device=dev)
+        else:
+            _check_like(where, "q_out", q_out, (b, n, hq, d), dtype, dev)
         k_out = None
         if isinstance(keys_out, torch.Tensor):
             k_out = keys_out
-            _on_device(where, dev, keys_out=k_out)
+            _check_like(where, "keys_out", k_out, (b, n, hk, d), dtype, dev)
         elif keys_out:
-            k_out = torch.empty(b, n, cache.kv_heads, cb.head_dim, dtype=k.dtype, device=dev)
-        for name, t, h in (("q_out", q_out, 0 if q is None else q.shape[1]), ("keys_out", k_out, cache.kv_heads)):
-            if t is not None and (t.shape != (b, n, h, cb.head_dim) or t.dtype != k.dtype or not t.is_contiguous()):
-                raise ValueError(f"{where}: {name} must be a contiguous {k.dtype} tensor {(b, n, h, cb.head_dim)}")
-        cs, rs = cache.struct(), rope.struct()
-        _check(lib.tq_rope_append(cb.handle, cs, rs, hq, 0 if q is None else q.shape[1], hk, hv, code, n,
-                                  _ptr(positions), int(bool(relative)), _ptr(start), _ptr(q_out), _ptr(k_out), s),
-               where)
+            k_out = torch.empty((b, n, hk, d), dtype=dtype, device=dev)
+        _check(lib.tq_rope_append(cb.handle, cs, rope.struct(), qv, hq, kv, vv, code, n, pos, int(bool(relative)), begin,
+                                  _ptr(q_out), _ptr(k_out), s), where)
     return q_out, k_out
+
+
+def _check_like(where: str, name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device):
+    if t.device != device:
+        _refuse_device(where, name, t, device)
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor {tuple(shape)}")
 
 
 def pack_tree_mask(sees: torch.Tensor) -> torch.Tensor:
@@ -560,30 +597,34 @@ def tq_tree_attention(cb: Codebook, cache: Cache, q: torch.Tensor, mask: torch.T
     where, dev = "tq_tree_attention", cache.seq_lens.device
     if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != cb.head_dim or not q.is_contiguous():
         raise ValueError(f"{where}: q must be contiguous [batch, n_q, q_heads, head_dim]")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{where}: q must be bfloat16 or float16, not {q.dtype}")
-    b, n, hq, _ = q.shape
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"{where}: q must be bfloat16 or float16, not {dtype}")
+    if q.device != dev or dev.type != "cuda":
+        _refuse_device(where, "q" if dev.type == "cuda" else "cache", q, dev)
+    b, n, hq, _ = shape = q.shape
     max_ctx = cache.capacity if max_ctx is None else max_ctx
-    _on_device(where, dev, cache=cache.seq_lens, q=q, mask=mask, out=out, workspace=workspace)
-    _check_cache(where, cb, cache, dev)
-    stride = 0
+    bits, stride = None, 0
     if mask is not None:
         words = (n + 31) // 32
-        _index_tensor(where, "mask", mask, (n, words) if mask.dim() == 2 else (b, n, words))
+        bits = _index_ptr(where, "mask", mask, (n, words) if mask.dim() == 2 else (b, n, words), dev)
         stride = 0 if mask.dim() == 2 else n * words
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
-        raise ValueError(f"{where}: out must be a contiguous {q.dtype} tensor {tuple(q.shape)}")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError(f"{where}: workspace must be contiguous")
+    cs = _cache_struct(where, cb, cache, dev)
     with _on(dev, stream) as s:
         if out is None:
             out = torch.empty_like(q)
+        else:
+            _check_like(where, "out", out, shape, dtype, dev)
         if workspace is None:
             need = tq_tree_workspace_bytes(cb, b, hq, cache.kv_heads, n, max_ctx)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check(lib.tq_tree_attention(cb.handle, cache.struct(), q.data_ptr(), _DTYPES[q.dtype], hq, n, _ptr(mask),
-                                     stride, float(softmax_scale), int(max_ctx), out.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), where)
+        elif workspace.device != dev:
+            _refuse_device(where, "workspace", workspace, dev)
+        elif not workspace.is_contiguous():
+            raise ValueError(f"{where}: workspace must be contiguous")
+        _check(lib.tq_tree_attention(cb.handle, cs, q.data_ptr(), _DTYPES[dtype], hq, n, bits, stride,
+                                     softmax_scale, max_ctx, out.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), s), where)
     return out
 
 
@@ -597,15 +638,14 @@ def tq_cache_compact(cb: Codebook, cache: Cache, index: torch.Tensor, counts: to
     if index.dim() not in (2, 3):
         raise ValueError(f"{where}: index must be [batch, n] or [batch, kv_heads, n]")
     n = index.shape[-1]
-    _on_device(where, dev, cache=cache.seq_lens, index=index, counts=counts, start=start)
-    _check_cache(where, cb, cache, dev)
-    _index_tensor(where, "index", index, (b, n) if index.dim() == 2 else (b, h, n))
-    _index_tensor(where, "counts", counts, (b,))
-    _index_tensor(where, "start", start, (b,))
-    sb, sh = (n, 0) if index.dim() == 2 else (h * n, n)
+    per_head = index.dim() == 3
+    cs = _cache_struct(where, cb, cache, dev)
+    at = _index_ptr(where, "index", index, (b, h, n) if per_head else (b, n), dev)
+    num = _index_ptr(where, "counts", counts, (b,), dev)
+    begin = _index_ptr(where, "start", start, (b,), dev)
     with _on(dev, stream) as s:
-        _check(lib.tq_cache_compact(cb.handle, cache.struct(), index.data_ptr(), sb, sh, counts.data_ptr(), n,
-                                    _ptr(start), s), where)
+        _check(lib.tq_cache_compact(cb.handle, cs, at, h * n if per_head else n, n if per_head else 0, num, n, begin, s),
+               where)
 
 
 def tq_cache_copy(cb: Codebook, dst: Cache, src: Cache, dst_rows: torch.Tensor, src_rows: torch.Tensor,
@@ -617,16 +657,13 @@ def tq_cache_copy(cb: Codebook, dst: Cache, src: Cache, dst_rows: torch.Tensor, 
     if dst_rows.dim() != 1:
         raise ValueError(f"{where}: dst_rows must be [n]")
     n = dst_rows.shape[0]
-    _on_device(where, dev, dst=dst.seq_lens, src=src.seq_lens, dst_rows=dst_rows, src_rows=src_rows,
-               lengths=lengths)
-    _check_cache(where, cb, dst, dev)
-    _check_cache(where, cb, src, dev)
-    for name, t in (("dst_rows", dst_rows), ("src_rows", src_rows), ("lengths", lengths)):
-        _index_tensor(where, name, t, (n,))
+    if src.seq_lens.device != dev:
+        _refuse_device(where, "src", src.seq_lens, dev)
+    cd = _cache_struct(where, cb, dst, dev)
+    cs = cd if src is dst else _cache_struct(where, cb, src, dev)
+    to = _index_ptr(where, "dst_rows", dst_rows, (n,), dev)
+    come = _index_ptr(where, "src_rows", src_rows, (n,), dev)
+    lens = _index_ptr(where, "lengths", lengths, (n,), dev)
     with _on(dev, stream) as s:
-        _check(lib.tq_cache_copy(cb.handle, dst.struct(), src.struct(), dst_rows.data_ptr(), src_rows.data_ptr(),
-                                 _ptr(lengths), n, src.capacity if max_len is None else int(max_len), s), where)
-
-
-def tq_free(cb: Codebook) -> None:
-    cb.__del__()
+        _check(lib.tq_cache_copy(cb.handle, cd, cs, to, come, lens, n, src.capacity if max_len is None else max_len, s),
+               where)
