@@ -174,6 +174,9 @@ class Codebook:
         _check(lib.tq_codebook_init(C.byref(self.params), C.byref(h), C.byref(self.layout)),
                "tq_codebook_init")
         self.handle = h
+        # elements of one slot: key codes, value codes, norms (or scales and biases), signs
+        lay = self.layout
+        self.slot_elements = (lay.k_code_bytes, lay.v_code_bytes, lay.norm_halves, lay.k_sign_bytes)
 
     @classmethod
     def from_kv_bits(cls, head_dim: int, kv_bits: float, qjl: bool = False, seed: int = 0,
@@ -450,24 +453,25 @@ def _index_ptr(where: str, name: str, t: torch.Tensor | None, shape: tuple, devi
 
 
 def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) -> tq_cache:
-    """The cache's arrays, which have the codebook's shapes and lie on its device."""
+    """The cache's arrays, each as large as the codebook asks for, contiguous and on
+    the cache's device."""
     if device.type != "cuda":
         _refuse_device(where, "cache", cache.seq_lens, device)
-    lay, n = cb.layout, (cache.batch, cache.kv_heads, cache.capacity)
-    meta = n + (lay.norm_halves,) if cb.affine else n
-    kc, vc, kn, vn = cache.k_codes, cache.v_codes, cache.k_norm, cache.v_norm
-    ks, kr = (cache.k_signs, cache.k_rnorm) if cb.qjl else (None, None)
+    index, (kb, vb, meta, sb) = device.index, cb.slot_elements
+    b, h, c = cache.batch, cache.kv_heads, cache.capacity
+    n = b * h * c
+    kc, vc, kn, vn, ks, kr = cache.k_codes, cache.v_codes, cache.k_norm, cache.v_norm, None, None
     sl, st, sy = cache.seq_lens, cache.status, cache.append_sync
-    want = ((kc, n + (lay.k_code_bytes,)), (vc, n + (lay.v_code_bytes,)), (kn, meta), (vn, meta),
-            (sl, n[:1]), (st, (1,)), (sy, n[:1]))
-    if cb.qjl:
-        want += ((ks, n + (lay.k_sign_bytes,)), (kr, n))
-    for t, shape in want:
-        if t is None or t.shape != shape or t.device != device or not t.is_contiguous():
+    want = ((kc, n * kb), (vc, n * vb), (kn, n * meta), (vn, n * meta), (sl, b), (st, 1), (sy, b))
+    if sb:
+        ks, kr = cache.k_signs, cache.k_rnorm
+        want += ((ks, n * sb), (kr, n))
+    for t, count in want:
+        if t is None or t.numel() != count or t.get_device() != index or not t.is_contiguous():
             name = next(k for k, v in vars(cache).items() if v is t)
-            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor {shape} on {device}")
-    return tq_cache(kc.data_ptr(), vc.data_ptr(), _ptr(ks), kn.data_ptr(), vn.data_ptr(), _ptr(kr), sl.data_ptr(),
-                    st.data_ptr(), sy.data_ptr(), *n)
+            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor of {count} elements on {device}")
+    return tq_cache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr() if sb else None, kn.data_ptr(), vn.data_ptr(),
+                    kr.data_ptr() if sb else None, sl.data_ptr(), st.data_ptr(), sy.data_ptr(), b, h, c)
 
 
 class Rope:
