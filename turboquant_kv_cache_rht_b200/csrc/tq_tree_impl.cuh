@@ -50,7 +50,7 @@ namespace tq {
 constexpr int kTile = 128;          // tokens per tile: the matrix instruction's rows
 constexpr int kTreeMaxCtas = 148;   // one block per SM; the workspace is sized for it
 constexpr int kMetaSlots = 4;       // tiles whose norms are in flight
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 8;
 // Slack of the running maximum (log2): weights stay below 2^14, fp16 holds 2^16,
 // and 2^-14 of the largest is still a normal number.  A key that resembles the
 // query outscores the others by about 2^13 at head_dim 128, so that a slack of 8
@@ -81,8 +81,8 @@ constexpr int kSegs = 4;  // segments announced ahead
 constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarStFull = 2, kBarStEmpty = kBarStFull + kMaxStages,
               kBarKFull = kBarStEmpty + kMaxStages, kBarKEmpty = kBarKFull + 2, kBarVFull = kBarKEmpty + 2,
               kBarVEmpty = kBarVFull + 2, kBarSFull = kBarVEmpty + 2, kBarSEmpty = kBarSFull + 2,
-              kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarMetaFull = kBarPEmpty + 2,
-              kBarMetaEmpty = kBarMetaFull + kMetaSlots, kBarSegFull = kBarMetaEmpty + kMetaSlots,
+              kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarMetaEmpty = kBarPEmpty + 2,
+              kBarSegFull = kBarMetaEmpty + kMetaSlots,
               kBarSegEmpty = kBarSegFull + kSegs, kBarDone = kBarSegEmpty + kSegs, kBars = kBarDone + 2;
 constexpr int kMiscTmem = kBars * 8, kMiscDead = kMiscTmem + 4,
               kMiscSeg = (kMiscTmem + 8 + 31) / 32 * 32,  // [kSegs][8] ints
@@ -96,7 +96,7 @@ __device__ __forceinline__ int bar_count(int i, int softmax_warps, int unpack_wa
   if (i >= kBarStEmpty && i < kBarKFull) return 2 * unpack_warps;
   if ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty)) return unpack_warps;
   if (i >= kBarSEmpty && i < kBarPEmpty) return softmax_warps;  // and kBarPFull
-  if (i >= kBarMetaFull && i < kBarMetaEmpty) return 4;
+  if (i >= kBarSFull && i < kBarSEmpty) return 2;               // the products, and the warp that issued them
   if (i >= kBarMetaEmpty && i < kBarSegFull) return softmax_warps;
   if (i >= kBarSegEmpty && i < kBarDone) return softmax_warps + 2 * unpack_warps + 3;  // all but the announcer
   return 1;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
     const float post0 = ta.scale * 1.4426950408889634f / (AFF ? sqrtf((float)D) : (float)D * tb.k_lam);
     const int live_rows = ta.n_q << ta.log_group, words = (ta.n_q + 31) >> 5;
     const int units = cv.kv_heads * pl.blocks;
-    float l[CPT][2 * NJ];  // this thread's part of the sums; the current chunk's first
+    float l[CPT][2 * NJ];  // this thread's part of the sums
     uint32_t n_tiles = 0;  // tiles of all segments before this one
     int buf = 0, ph = 0;   // score and weight buffer, its phase
     pdl_wait();
@@ -378,23 +378,22 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
         const uint32_t tile_no = n_tiles + it;
         const int slot = tile_no % kMetaSlots, tok0 = sg.t0 + it * kTile + 32 * w + g;
         const bool masked = sg.t0 + (it + 1) * kTile > ctx;
-        fail = !tm::mbar_wait(bar(kBarMetaFull + slot), (tile_no / kMetaSlots) & 1, dead) || fail;
         float kn[4], vn[4], ev[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a = pl.sm_meta + slot * 1536 + 4 * (32 * w + 8 * k + g);
-          kn[k] = tm::ldsf(a) * post;
-          vn[k] = tm::ldsf(a + 512);
-          ev[k] = tm::ldsf(a + 1024);
-        }
-        __syncwarp();
-        if (lane == 0) tm::mbar_arrive(bar(kBarMetaEmpty + slot));
-#pragma unroll 1
         for (int chunk = 0; chunk < CPT; ++chunk) {
           const int col0 = chunk * CN + part;  // of the outputs and of the maxima
           const uint32_t t_s = tmem + pl.tm_s + buf * CN + part + lanes;
           fail = !tm::mbar_wait(bar(kBarSFull + buf), ph, dead) || fail;
           tm::fence_after();
+          if (CPT == 1 || chunk == 0) {  // the tile's norms, which were there before its keys were
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a = pl.sm_meta + slot * 1536 + 4 * (32 * w + 8 * k + g);
+              kn[k] = tm::ldsf(a) * post;
+              vn[k] = tm::ldsf(a + 512);
+              ev[k] = tm::ldsf(a + 1024);
+            }
+          }
           float y[8 * NJ];
           uint32_t vis = 0xffffffffu;
           if (__builtin_expect(masked, 0))
@@ -413,8 +412,8 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {
                 const uint2 x = tm::lds64(sm_al + 4 * (8 * j + 2 * qd));
-                l[0][2 * j] *= __uint_as_float(x.x);
-                l[0][2 * j + 1] *= __uint_as_float(x.y);
+                l[chunk][2 * j] *= __uint_as_float(x.x);
+                l[chunk][2 * j + 1] *= __uint_as_float(x.y);
               }
             }
             float2 m2[NJ];
@@ -459,14 +458,14 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           tm::fence_before();
           __syncwarp();
           if (lane == 0) tm::mbar_arrive(bar(kBarSEmpty + buf));
-          fail = !tm::mbar_wait(bar(kBarPEmpty + buf), ph ^ 1, dead) || fail;
+          if (pl.nsb == 1) fail = !tm::mbar_wait(bar(kBarPEmpty + buf), ph ^ 1, dead) || fail;  // (else the scores waited)
           // weight buffers: blocks of 64 columns, or halves of one when narrower
           const uint32_t sm_p = pl.sm_p + (CN >= 64 ? buf * (CN / 64) + part / 64 : 0) * 16384 + (32 * w + lane) * 128;
           const int piece = CN >= 64 ? part % 64 / 8 : 4 * buf + part / 8;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             uint32_t pk[4];
-            float2 sum = make_float2(l[0][2 * j], l[0][2 * j + 1]);
+            float2 sum = make_float2(l[chunk][2 * j], l[chunk][2 * j + 1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int i = y_at<NJ>(k, j);
@@ -476,23 +475,18 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
               const __half2 hw = __floats2half2_rn(wt.x, wt.y);
               pk[k] = *reinterpret_cast<const uint32_t*>(&hw);
             }
-            l[0][2 * j] = sum.x;
-            l[0][2 * j + 1] = sum.y;
+            l[chunk][2 * j] = sum.x;
+            l[chunk][2 * j + 1] = sum.y;
             tm::stmatrix_x4(sm_p + (((piece + j) ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
           tm::fence_proxy_async();
           tm::fence_before();
           __syncwarp();
-          if (lane == 0) tm::mbar_arrive(bar(kBarPFull + buf));
-          if (++buf == pl.nsb) buf = 0, ph ^= 1;
-          if constexpr (CPT == 2) {  // the other chunk's sums come to the front (registers have no index)
-#pragma unroll
-            for (int j = 0; j < 2 * NJ; ++j) {
-              const float x = l[0][j];
-              l[0][j] = l[1][j];
-              l[1][j] = x;
-            }
+          if (lane == 0) {
+            tm::mbar_arrive(bar(kBarPFull + buf));
+            if (CPT == 1 || chunk == CPT - 1) tm::mbar_arrive(bar(kBarMetaEmpty + slot));
           }
+          if (++buf == pl.nsb) buf = 0, ph ^= 1;
         }
       }
       n_tiles += sg.tiles;
@@ -595,8 +589,6 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           tm::stsf(a_meta, kn);
           tm::stsf(a_meta + 512, vn);
           tm::stsf(a_meta + 1024, ev);
-          __syncwarp();
-          if (lane == 0) tm::mbar_arrive(bar(kBarMetaFull + slot));
         }
         // ---- channels, then signs
         tm::fence_after();
@@ -701,6 +693,8 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
 #pragma unroll 1
           for (int c = 0; c < CPT; ++c, bq += CN * 128 / 16) {
             fail = !tm::mbar_wait(bar(kBarSEmpty + buf), s_ph ^ 1, dead) || fail;
+            // two buffers: the weights' is free too once the scores are there
+            if (pl.nsb == 2) fail = !tm::mbar_wait(bar(kBarPEmpty + buf), s_ph ^ 1, dead) || fail;
             tm::fence_after();
             const uint32_t d = tmem + pl.tm_s + buf * CN;
             if (lane == 0 && !fail) {
@@ -715,6 +709,7 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
                   tm::mma_ts(d, ap + 8 * k, b + (k >> 2) * q_blk + 2 * (k & 3), d_hi, id, 1);
               }
               tm::mma_commit(bar(kBarSFull + buf));
+              tm::mbar_arrive(bar(kBarSFull + buf));  // (passes on what this warp saw of the keys' warps: the norms)
               if (c == CPT - 1) {
                 tm::mma_commit(bar(kBarKEmpty + kb));
                 if (t == sg.tiles - 1) tm::mma_commit(bar(kBarQEmpty));
