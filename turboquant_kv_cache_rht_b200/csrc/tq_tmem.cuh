@@ -269,11 +269,11 @@ __device__ __forceinline__ uint32_t lds_half(uint32_t a) {
 __device__ __forceinline__ void stsf(uint32_t a, float x) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint16_t x) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(x) : "memory");
 }
 
 }  // namespace tm

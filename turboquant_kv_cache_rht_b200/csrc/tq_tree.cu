@@ -304,7 +304,7 @@ bool plan_shape(const Tables& tb, int dtype, int cn, int chunks, int nkb, int nv
   p->st_rn = part(tb.qjl ? 2 : 0);
   p->st_bytes = (at + 127) / 128 * 128;
   p->sm_st = a.take(nst * p->st_bytes, 128);
-  p->sm_meta = a.take(kMetaSlots * 3 * kTile * 4, 128);
+  p->sm_meta = a.take(kMetaSlots * kTile * 8, 128);
   p->sm_misc = a.take(kMiscBytes, 16);
   // at least half of an SM's shared memory: one block per SM, which owns its tensor memory
   p->smem = std::max(a.end - (int)kDynSmemBase, 120 * 1024);

@@ -49,7 +49,10 @@ namespace tq {
 
 constexpr int kTile = 128;          // tokens per tile: the matrix instruction's rows
 constexpr int kTreeMaxCtas = 148;   // one block per SM; the workspace is sized for it
-constexpr int kMetaSlots = 4;       // tiles whose norms are in flight
+// Tiles whose norms are kept.  A slot is written for tile t when the scores of t - 2
+// (at most two key buffers) are done; their buffer had been given back by then, by
+// warps that had finished tile t - 5 or a later one: six slots need no barrier.
+constexpr int kMetaSlots = 6;
 constexpr int kMaxStages = 8;
 // Slack of the running maximum (log2): weights stay below 2^14, fp16 holds 2^16,
 // and 2^-14 of the largest is still a normal number.  A key that resembles the
@@ -81,8 +84,7 @@ constexpr int kSegs = 4;  // segments announced ahead
 constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarStFull = 2, kBarStEmpty = kBarStFull + kMaxStages,
               kBarKFull = kBarStEmpty + kMaxStages, kBarKEmpty = kBarKFull + 2, kBarVFull = kBarKEmpty + 2,
               kBarVEmpty = kBarVFull + 2, kBarSFull = kBarVEmpty + 2, kBarSEmpty = kBarSFull + 2,
-              kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarMetaEmpty = kBarPEmpty + 2,
-              kBarSegFull = kBarMetaEmpty + kMetaSlots,
+              kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarSegFull = kBarPEmpty + 2,
               kBarSegEmpty = kBarSegFull + kSegs, kBarDone = kBarSegEmpty + kSegs, kBars = kBarDone + 2;
 constexpr int kMiscTmem = kBars * 8, kMiscDead = kMiscTmem + 4,
               kMiscSeg = (kMiscTmem + 8 + 31) / 32 * 32,  // [kSegs][8] ints
@@ -97,7 +99,6 @@ __device__ __forceinline__ int bar_count(int i, int softmax_warps, int unpack_wa
   if ((i >= kBarKFull && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty)) return unpack_warps;
   if (i >= kBarSEmpty && i < kBarPEmpty) return softmax_warps;  // and kBarPFull
   if (i >= kBarSFull && i < kBarSEmpty) return 2;               // the products, and the warp that issued them
-  if (i >= kBarMetaEmpty && i < kBarSegFull) return softmax_warps;
   if (i >= kBarSegEmpty && i < kBarDone) return softmax_warps + 2 * unpack_warps + 3;  // all but the announcer
   return 1;
 }
@@ -127,43 +128,67 @@ __device__ __forceinline__ bool next_segment(uint32_t misc, uint32_t& n, Segment
   return __all_sync(0xffffffffu, s.tiles > 0 && !fail);
 }
 
-// 32 channels of a packed row at shared address `row` -> 16 fp16 pairs.
-template <int BITS>
-__device__ __forceinline__ void unpack32(uint32_t row, uint32_t lut, uint32_t (&r)[16]) {
-  if constexpr (BITS == 2) {
-    const uint2 w = tm::lds64(row);
+// f(block, pairs) for each of N blocks of 32 channels of a packed row at shared
+// address `row`: 16 fp16 pairs from the table.  The row's words are loaded first.
+template <int N, int BITS, bool WIDE, typename F>
+__device__ __forceinline__ void unpack_row(uint32_t row, uint32_t lut, F f) {
+  uint32_t w[N * BITS];
+  if constexpr (WIDE && N * BITS % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // a byte of four codes, entries 128 bytes apart
-      const uint2 x = tm::lut64(bits_at(i < 4 ? w.x : w.y, 8 * (i & 3), 8, 7) | lut);
-      r[2 * i] = x.x;
-      r[2 * i + 1] = x.y;
+    for (int i = 0; i < N * BITS / 4; ++i) {
+      const uint4 x = tm::lds128(row + 16 * i);
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
     }
-  } else if constexpr (BITS == 3) {
-    const uint32_t w[3] = {tm::lds32(row), tm::lds32(row + 4), tm::lds32(row + 8)};
+  } else if constexpr (N * BITS % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = tm::lut32(field_scaled(w, 3, 6 * i, 6, 7) | lut);
+    for (int i = 0; i < N * BITS / 2; ++i) {
+      const uint2 x = tm::lds64(row + 8 * i);
+      w[2 * i] = x.x;
+      w[2 * i + 1] = x.y;
+    }
   } else {
-    const uint4 w = tm::lds128(row);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t x = i < 4 ? w.x : i < 8 ? w.y : i < 12 ? w.z : w.w;
-      r[i] = tm::lut32(bits_at(x, 8 * (i & 3), 8, 6) | lut);
-    }
+    for (int i = 0; i < N * BITS; ++i) w[i] = tm::lds32(row + 4 * i);
   }
-}
-
-// f(block, pairs) for every 32 channels of a row, or of half of it.  The loop stays rolled: the
-// roles share the instruction caches, and unrolled roles starved
-// each other (two thirds of the stalls were for instructions).
-template <int N, int BITS, typename F>
-__device__ __forceinline__ void unpack_row(uint32_t row, uint32_t lut, int half, F f) {
-#pragma unroll 1
-  for (int c = half * N; c < (half + 1) * N; ++c) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
     uint32_t r[16];
-    unpack32<BITS>(row + 4 * BITS * c, lut, r);
+    const uint32_t* x = w + BITS * c;
+    if constexpr (BITS == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // a byte of four codes, entries 128 bytes apart
+        const uint2 y = tm::lut64(bits_at(x[i >> 2], 8 * (i & 3), 8, 7) | lut);
+        r[2 * i] = y.x;
+        r[2 * i + 1] = y.y;
+      }
+    } else if constexpr (BITS == 3) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = tm::lut32(field_scaled(x, 3, 6 * i, 6, 7) | lut);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = tm::lut32(bits_at(x[i >> 2], 8 * (i & 3), 8, 6) | lut);
+    }
     f(c, r);
   }
 }
+
+// The same, in a rolled loop if ROLLED: beside the softmax of two wide chunks the
+// unrolled one costs more in instruction fetches than it gains (gqa 32k 78 us
+// instead of 74; with one chunk it gains: 4 x 128k with the sketch 450 -> 421 us).
+template <bool ROLLED, int N, int BITS, bool WIDE, typename F>
+__device__ __forceinline__ void unpack_blocks(uint32_t row, uint32_t lut, F f) {
+  if constexpr (ROLLED) {
+#pragma unroll 1
+    for (int c = 0; c < N; ++c)
+      unpack_row<1, BITS, WIDE>(row + 4 * BITS * c, lut, [&](int, uint32_t (&r)[16]) { f(c, r); });
+  } else {
+    unpack_row<N, BITS, WIDE>(row, lut, f);
+  }
+}
+
 // Fills a table with every lane's copy of every entry.
 __device__ __forceinline__ void fill_lut(uint32_t lut, int bits, const float* cent, float lam) {
   const uint32_t mask = (1u << bits) - 1u;
@@ -281,27 +306,30 @@ __device__ __forceinline__ bool raise_max(const Raise& a, const float (&kn)[4], 
   return ok;
 }
 
-// Warps of a kernel: softmax, keys (values as many), and the four others.  Wide
-// chunks keep the softmax busiest: four warpgroups, 32 columns apiece.  Narrow ones
-// wait for the codes: two warpgroups unpack each side, half a row apiece.
-template <int CN>
+// Warps of a kernel: softmax (a warpgroup per 16 or 32 columns), keys (values as
+// many), and the four others.  At head_dim 256 a second warpgroup unpacks each side,
+// half a row apiece (157 us instead of 169 at 8 drafts and 200k); at 128 it gains
+// nothing over fewer, larger warps.
+template <int D, int CN>
 struct Roles {
-  static constexpr int SW = CN == 128 ? 16 : CN == 16 ? 4 : 8, KW = CN == 128 ? 4 : 8;
-  static constexpr int THREADS = 32 * (SW + 2 * KW + 4);
-  // registers: moved to the softmax from what the block is launched with (72 of each
-  // of 7 warpgroups, or 80 of 6): 4 x 88 + 56 + 56 + 40 = 504; 2 x 128 + 4 x 48 + 48 =
-  // 496; 128 + 4 x 64 + 56 = 440 of 480
-  static constexpr int RS = CN == 128 ? 88 : 128, RU = CN == 128 ? 56 : CN == 16 ? 64 : 48,
-                       RO = CN == 128 ? 40 : CN == 16 ? 56 : 48;
+  static constexpr int SW = D < 256 && CN >= 64 ? 16 : CN == 16 ? 4 : 8, KW = D == 256 ? 8 : 4;
+  static constexpr int WARPS = SW + 2 * KW + 4, THREADS = 32 * WARPS;
+  // registers of a softmax, an unpacking and another thread: moved from what the block
+  // is launched with, 72, 80, 96 or 128 for each of 7, 6, 5 or 4 warpgroups
+  static constexpr int RS = SW == 16 ? 88 : 128, RU = WARPS == 28 ? (SW == 16 ? 56 : 48) : WARPS == 24 ? 64 : WARPS == 20 ? 72 : 96,
+                       RO = SW == 16 ? 40 : WARPS == 28 ? 48 : WARPS == 24 ? 56 : WARPS == 20 ? 56 : 64;
+  static constexpr int LAUNCH = WARPS == 28 ? 72 : WARPS == 24 ? 80 : WARPS == 20 ? 96 : 128;
+  static_assert(SW * RS + 2 * KW * RU + 4 * RO <= WARPS * LAUNCH, "the shares' sum is within the launch's registers");
 };
 
 template <int D, int CN, int CPT, int KB, int VB, bool QJL, bool AFF>
-__global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
+__global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
     tree_kernel(const __grid_constant__ Tables tb, const __grid_constant__ CacheView cv,
                 const __grid_constant__ TreeArgs ta, const __grid_constant__ TreePlan pl, uint8_t* __restrict__ ws) {
-  using R = Roles<CN>;
+  using R = Roles<D, CN>;
   constexpr int SW = R::SW, KW = R::KW, OW = SW + 2 * KW;  // OW: the first of the others
   constexpr int SUB = CN / (SW / 4), NJ = SUB / 8;         // columns of a warpgroup
+  constexpr int N = D / 8 / KW;                            // blocks of 32 channels that a thread unpacks
   constexpr int MB = D == 256 ? 2 : 1;     // 128-channel blocks of the output
   constexpr int NG = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -375,8 +403,7 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
 
 #pragma unroll 1
       for (int it = 0; it < sg.tiles; ++it) {
-        const uint32_t tile_no = n_tiles + it;
-        const int slot = tile_no % kMetaSlots, tok0 = sg.t0 + it * kTile + 32 * w + g;
+        const int slot = (n_tiles + it) % kMetaSlots, tok0 = sg.t0 + it * kTile + 32 * w + g;
         const bool masked = sg.t0 + (it + 1) * kTile > ctx;
         float kn[4], vn[4], ev[4];
 #pragma unroll
@@ -388,10 +415,10 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           if (CPT == 1 || chunk == 0) {  // the tile's norms, which were there before its keys were
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t a = pl.sm_meta + slot * 1536 + 4 * (32 * w + 8 * k + g);
-              kn[k] = tm::ldsf(a) * post;
-              vn[k] = tm::ldsf(a + 512);
-              ev[k] = tm::ldsf(a + 1024);
+              const uint2 x = tm::lds64(pl.sm_meta + slot * 1024 + 8 * (32 * w + 8 * k + g));
+              kn[k] = __uint_as_float(x.x) * post;
+              vn[k] = __uint_as_float(x.y);
+              ev[k] = fast_log2(vn[k] + 0x1p-30f);  // a zero norm gives -30
             }
           }
           float y[8 * NJ];
@@ -458,7 +485,7 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           tm::fence_before();
           __syncwarp();
           if (lane == 0) tm::mbar_arrive(bar(kBarSEmpty + buf));
-          if (pl.nsb == 1) fail = !tm::mbar_wait(bar(kBarPEmpty + buf), ph ^ 1, dead) || fail;  // (else the scores waited)
+          fail = !tm::mbar_wait(bar(kBarPEmpty + buf), ph ^ 1, dead) || fail;
           // weight buffers: blocks of 64 columns, or halves of one when narrower
           const uint32_t sm_p = pl.sm_p + (CN >= 64 ? buf * (CN / 64) + part / 64 : 0) * 16384 + (32 * w + lane) * 128;
           const int piece = CN >= 64 ? part % 64 / 8 : 4 * buf + part / 8;
@@ -484,7 +511,6 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             tm::mbar_arrive(bar(kBarPFull + buf));
-            if (CPT == 1 || chunk == CPT - 1) tm::mbar_arrive(bar(kBarMetaEmpty + slot));
           }
           if (++buf == pl.nsb) buf = 0, ph ^= 1;
         }
@@ -544,13 +570,12 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
         const int slot = n % kMetaSlots;
         const uint32_t stage = pl.sm_st + st * pl.st_bytes;
         fail = !tm::mbar_wait(bar(kBarStFull + st), st_ph, dead);
-        fail = !tm::mbar_wait(bar(kBarMetaEmpty + slot), ((n / kMetaSlots) & 1) ^ 1, dead) || fail;
         fail = !tm::mbar_wait(bar(kBarKEmpty + kb), k_ph ^ 1, dead) || fail;
         fail = __any_sync(0xffffffffu, fail);
         if (fail) break;
         const bool valid = sg.t0 + it * kTile + tok < sg.len;
         // ---- the token's norms
-        float kn = 1.f, vn, ev = 0.f, ratio = 0.f;
+        float kn = 1.f, vn, ratio = 0.f;
         if (AFF) {
           uint32_t f = 1u;  // largest fp16 exponent field among the value's |scale|, |bias|
 #pragma unroll
@@ -559,13 +584,11 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
             f = max(f, max((x >> 10) & 31u, (x >> 26) & 31u));
           }
           const int e = min((int)f, 29) - 15;
-          ev = valid ? (float)e : 0.f;
           vn = !valid ? 0.f : f == 31u ? __int_as_float(0x7fffffff) : __int_as_float((e + 127) << 23);
         } else {
           const uint32_t a = tm::lds_half(stage + pl.st_kn + 2 * tok), b = tm::lds_half(stage + pl.st_vn + 2 * tok);
           kn = __half2float(__ushort_as_half((uint16_t)a));
           vn = valid ? __half2float(__ushort_as_half((uint16_t)b)) : 0.f;
-          ev = valid ? fast_log2(vn + 0x1p-30f) : 0.f;
         }
         if (QJL) {
           // the sketch enters the reduction as its ratio to the key's norm; a norm below
@@ -585,15 +608,13 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           kn = __int_as_float(0x7fffffff);
         }
         if (half == 0) {
-          const uint32_t a_meta = pl.sm_meta + slot * 1536 + 4 * tok;
-          tm::stsf(a_meta, kn);
-          tm::stsf(a_meta + 512, vn);
-          tm::stsf(a_meta + 1024, ev);
+          tm::sts64(pl.sm_meta + slot * 1024 + 8 * tok, __float_as_uint(kn), __float_as_uint(vn));
         }
         // ---- channels, then signs
         tm::fence_after();
         const uint32_t dst = tmem + pl.tm_k + kb * pl.kcols + ((uint32_t)(32 * w) << 16);
-        unpack_row<D / 8 / KW, KB>(stage + tok * row_bytes, lut, half, [&](int c, uint32_t (&r)[16]) {
+        unpack_blocks<CPT == 2, N, KB, D * KB % 128 == 0>(stage + tok * row_bytes + half * (N * KB * 4), lut, [&](int ci, uint32_t (&r)[16]) {
+          const int c = half * N + ci;
           if (AFF) {
             const uint32_t x = tm::lds32(stage + pl.st_kn + (tok * NG + (c >> 1)) * 4);
             const uint32_t s = __byte_perm(x, x, 0x1010), b = __byte_perm(x, x, 0x3232);
@@ -605,7 +626,7 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
         if (QJL) {
           const uint32_t rr = pack_half2(__float2half_rn(ratio), __float2half_rn(ratio));
 #pragma unroll 1
-          for (int c = half * (D / 8 / KW); c < (half + 1) * (D / 8 / KW); ++c) {
+          for (int c = half * N; c < (half + 1) * N; ++c) {
             const uint32_t x = ~tm::lds32(stage + pl.st_s + tok * (D / 8) + 4 * c);  // bit 1: +
             uint32_t r[16];
 #pragma unroll
@@ -652,7 +673,8 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
           mul |= mul << 16;
         }
         const uint32_t dst = pl.sm_v + vb * (kTile * D * 2) + tok * 128;
-        unpack_row<D / 8 / KW, VB>(stage + pl.st_v + tok * row_bytes, lut, half, [&](int c, uint32_t (&r)[16]) {
+        unpack_blocks<CPT == 2, N, VB, D * VB % 128 == 0>(stage + pl.st_v + tok * row_bytes + half * (N * VB * 4), lut, [&](int ci, uint32_t (&r)[16]) {
+          const int c = half * N + ci;
           if (AFF) {
             const uint32_t x = hmul2_bits(tm::lds32(stage + pl.st_vn + (tok * NG + (c >> 1)) * 4), mul);
             const uint32_t s = __byte_perm(x, x, 0x1010), b = __byte_perm(x, x, 0x3232);
@@ -693,8 +715,6 @@ __global__ void __launch_bounds__(Roles<CN>::THREADS, 1)
 #pragma unroll 1
           for (int c = 0; c < CPT; ++c, bq += CN * 128 / 16) {
             fail = !tm::mbar_wait(bar(kBarSEmpty + buf), s_ph ^ 1, dead) || fail;
-            // two buffers: the weights' is free too once the scores are there
-            if (pl.nsb == 2) fail = !tm::mbar_wait(bar(kBarPEmpty + buf), s_ph ^ 1, dead) || fail;
             tm::fence_after();
             const uint32_t d = tmem + pl.tm_s + buf * CN;
             if (lane == 0 && !fail) {
@@ -888,9 +908,9 @@ cudaError_t launch_tree_shape(const Tables& tb, const CacheView& cv, const TreeA
   static KernelConfig config;
   auto kern = tree_kernel<D, CN, CPT, KB, VB, QJL, AFF>;
   // the attribute is set once per device, for the largest plan
-  cudaError_t e = configure_kernel(config, kern, 227 * 1024, Roles<CN>::THREADS, nullptr);
+  cudaError_t e = configure_kernel(config, kern, 227 * 1024, Roles<D, CN>::THREADS, nullptr);
   if (e != cudaSuccess) return e;
-  cfg->blockDim = dim3(Roles<CN>::THREADS);
+  cfg->blockDim = dim3(Roles<D, CN>::THREADS);
   return cudaLaunchKernelEx(cfg, kern, tb, cv, ta, pl, ws);
 }
 
