@@ -10,7 +10,9 @@ namespace {
 
 // ---- queries: rotated, scaled by a power of two, rounded to fp16, in the layout
 // of the product's B operand (128-byte rows of 64 channels, swizzled; blocks of
-// `rows` rows; parts hi, lo of an fp16 call, sketch).  One block per unit; the scale
+// `rows` rows; parts hi, lo of an fp16 call, sketch).  Grid: (units, shares of the
+// rows); every block reads all of the unit's rows for the scale (few units would
+// leave most SMs idle: one block per unit took 13 us for 8 units of 252 rows).  It
 // is common to its rows: |u| <= d max|q| is brought to 2^14, or 2^10 before the
 // second rotation, which can add sqrt(d).  Rows that are not finite do not count.
 constexpr int kPrepThreads = 1024;
@@ -74,11 +76,11 @@ __global__ void __launch_bounds__(kPrepThreads)
   int ex = 0;
   frexpf(amax > 0.f ? amax * D : 1.f, &ex);
   const float scale = ldexpf(1.f, max(min((tb.qjl ? 10 : 14) - ex, 100), -100));
-  if (tid == 0) reinterpret_cast<float*>(ws + pl.ws_scale)[unit] = scale;
+  if (tid == 0 && blockIdx.y == 0) reinterpret_cast<float*>(ws + pl.ws_scale)[unit] = scale;
   uint8_t* table = ws + pl.ws_q + (long)unit * pl.q_bytes;
   const int blk = pl.rows * 128, part = pl.rows * D * 2;
 #pragma unroll 1
-  for (int rr = warp; rr < pl.rows; rr += 32) {
+  for (int rr = 32 * blockIdx.y + warp; rr < pl.rows; rr += 32 * gridDim.y) {
     float u[E];
     if (rr < rows) {
       load(rr, u);
@@ -381,7 +383,9 @@ cudaError_t launch_dim(const Tables& tb, const CacheView& cv, const TreeArgs& ta
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3((unsigned)(pl.slots - pl.ctas));
+  // shares of 32 rows, until there is a block for each SM
+  const long units = pl.slots - pl.ctas;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)std::max(1L, std::min((pl.rows + 31) / 32L, kTreeMaxCtas / units)));
   cfg.blockDim = dim3(kPrepThreads);
   cudaError_t e = cudaLaunchKernelEx(&cfg, tree_query_kernel<D>, tb, cv, ta, pl, ws);
   if (e != cudaSuccess) return e;
