@@ -64,8 +64,9 @@ typedef enum {
 /* Sticky device-side flags ORed into *tq_cache.status. */
 #define TQ_FLAG_CAPACITY 1u  /* an append would pass `capacity`: that batch row was skipped */
 #define TQ_FLAG_MAXCTX 2u    /* a sequence was longer than the decode's max_ctx: its tail was not attended */
-#define TQ_FLAG_LAYOUT 4u    /* the decode kernel found its shared memory placed other than the host
-                                checked (never expected on sm_100a): its outputs are not valid */
+#define TQ_FLAG_LAYOUT 4u    /* the decode or the tree attention found its shared (or tensor) memory
+                                placed other than the host checked (never expected on sm_100a): its
+                                outputs are not valid */
 #define TQ_FLAG_INDEX 8u     /* a position, slot or row given on the device was out of range or in
                                 conflict with another: see the call that took it */
 #define TQ_FLAG_TIMEOUT 16u  /* the tree attention gave up a wait inside a kernel (never expected):
@@ -409,10 +410,14 @@ size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, in
  * mask : DEVICE uint32 words, bit j % 32 of word j / 32 of row i: draft i attends
  *        draft j; [n_q][ceil(n_q / 32)] per batch row, mask_stride words apart
  *        (0: one mask for every row).  NULL: a chain, j <= i.
- * out  : DEVICE `dtype`, like q.  Its operands are 16-bit: scores and weights are
- *        accumulated in fp32, the weights and the rotated queries rounded to fp16.
+ * out  : DEVICE `dtype`, like q.
+ * The products' operands are fp16, their sums, the scores, maxima and sums fp32: the
+ * weights are rounded to fp16, and so are the rotated queries of a bf16 call (an
+ * fp16 call holds them in two parts, 22 bits) and the affine codec's keys and values.
  * A draft that attends nothing gives zeros, as do all drafts of a row that holds
- * fewer than n_q tokens.  softmax_scale, max_ctx, workspace: as for
+ * fewer than n_q tokens.  What a draft does not attend never reaches it, whatever
+ * the cache holds there; a token whose value has no finite norm (or scale, or bias)
+ * makes the drafts that attend it NaN.  softmax_scale, max_ctx, workspace: as for
  * tq_decode_attention (tokens at max_ctx and past it, drafts among them, are not
  * attended and set TQ_FLAG_MAXCTX).  q_heads / kv_heads is 1, 2, 4 or 8 and the
  * code widths are those of the decode.  The result is deterministic. */

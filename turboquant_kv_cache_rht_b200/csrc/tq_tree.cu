@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int units = H * pl.blocks, nctas = pl.ctas;
   long long before = 0, all = 0;
   for (int k = tid; k < cv.batch; k += NT) {
-    const long long x = tree_tiles(cv, k, ta.n_q, ta.max_ctx);
+    const long long x = tree_span(cv, k, ta.n_q, ta.max_ctx);
     all += x;
     before += k < b ? x : 0;
   }
@@ -159,9 +159,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     all += tiles[0][w];
     before += tiles[1][w];
   }
-  const int n = tree_tiles(cv, b, ta.n_q, ta.max_ctx);
+  const int n = tree_span(cv, b, ta.n_q, ta.max_ctx);
   const long out_at = (((long)b * ta.n_q + i) * ta.q_heads + h) * D;
-  const long long T = all * units, unit = (long long)kvh * pl.blocks + rb, su = before * units + unit * n, eu = su + n;
+  // the unit's tiles are [su, eu) of the T places
+  const long long T = all * units, unit = (long long)kvh * pl.blocks + rb, eu = before * units + (unit + 1) * n,
+                  su = eu - max(n - kUnitCost, 0);
   const int c_lo = n > 0 ? (int)(((su + 1) * nctas + T - 1) / T - 1) : 0;
   const int c_hi = n > 0 ? (int)((eu * nctas + T - 1) / T - 1) : -1;
   const int S = c_hi - c_lo + 1;

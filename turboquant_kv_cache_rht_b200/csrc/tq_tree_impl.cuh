@@ -112,8 +112,14 @@ __device__ __forceinline__ int tree_len(const CacheView& cv, int b, int n_q, int
   const int stored = min(max(cv.seq_lens[b], 0), cv.capacity);
   return stored < n_q ? 0 : min(stored, max_ctx);
 }
-__device__ __forceinline__ int tree_tiles(const CacheView& cv, int b, int n_q, int max_ctx) {
-  return (tree_len(cv, b, n_q, max_ctx) + kTile - 1) / kTile;
+// What a unit of `tiles` tiles counts for in the blocks' shares: its tiles, and a few
+// more for what a segment costs besides (the queries' copy, the pipeline's filling,
+// the partial's stores: about 9000 cycles, a tile takes 2500 to 6000).  Without them a
+// block with many short rows took 1.2 times the average (16 ragged rows).
+constexpr int kUnitCost = 3;
+__device__ __forceinline__ int tree_span(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+__device__ __forceinline__ int tree_span(const CacheView& cv, int b, int n_q, int max_ctx) {
+  return tree_span((tree_len(cv, b, n_q, max_ctx) + kTile - 1) / kTile);
 }
 
 // The next announced segment; false at the end or when a wait gave up.
@@ -777,20 +783,20 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
       }
     } else if (warp == OW + 2) {
       // ========================= share, segments, packed tiles ===============
-      // This block takes tiles [t, t1) of the T laid end to end over all units.
+      // This block takes [t, t1) of the units' spans, T laid end to end.
       const int n_q = ta.n_q, max_ctx = ta.max_ctx, units = cv.kv_heads * pl.blocks;
       long long T = 0;
-      for (int r = lane; r < cv.batch; r += 32) T += tree_tiles(cv, r, n_q, max_ctx);
+      for (int r = lane; r < cv.batch; r += 32) T += tree_span(cv, r, n_q, max_ctx);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
       T *= units;
       long long t = tile_bound(blockIdx.x, T, gridDim.x);
       const long long t1 = tile_bound((long long)blockIdx.x + 1, T, gridDim.x);
-      long long rs = 0;  // tiles before row b
+      long long rs = 0;  // spans before row b
       int b = 0;
       for (; b < cv.batch && t < t1; b += 32) {
-        const int n = b + lane < cv.batch ? tree_tiles(cv, b + lane, n_q, max_ctx) : 0;
-        long long e = n;  // tiles up to and with this row
+        const int n = b + lane < cv.batch ? tree_span(cv, b + lane, n_q, max_ctx) : 0;
+        long long e = n;  // spans up to and with this row
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long x = __shfl_up_sync(0xffffffffu, e, o);
@@ -812,7 +818,7 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
         while (true) {
           Segment s{0, 0, 0, 0, 0};
           while (t < t1) {
-            const int len = tree_len(cv, b, n_q, max_ctx), n = (len + kTile - 1) / kTile;
+            const int len = tree_len(cv, b, n_q, max_ctx), n = tree_span((len + kTile - 1) / kTile);
             const long long row = (long long)n * units;
             if (t >= rs + row) {
               rs += row;
@@ -822,8 +828,11 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
             const long long at = t - rs;
             const int u = at < (1ll << 31) ? (int)((unsigned)at / (unsigned)n) : (int)(at / n);
             const long long us = rs + (long long)u * n, te = min(t1, us + n);
-            s = Segment{b, u, (int)(t - us) * kTile, (int)(te - t), len};
+            // a unit's first places stand for its cost, its tiles follow
+            const int lo = max((int)(t - us) - kUnitCost, 0), hi = (int)(te - us) - kUnitCost;
             t = te;
+            if (hi <= lo) continue;
+            s = Segment{b, u, lo * kTile, hi - lo, len};
             break;
           }
           const uint32_t slot = seg_n % kSegs, a = misc + kMiscSeg + 32 * slot;
