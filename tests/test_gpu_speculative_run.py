@@ -4,7 +4,7 @@ float64 attention, the accepted path is kept, and the next step goes on from it.
 import pytest
 import torch
 
-from tests.spec_helpers import arrays, assert_tree_close, random_tree, tree_reference
+from tests.spec_helpers import arrays, assert_tree_close, decoded, random_tree, rotation, tree_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,70 @@ def test_draft_verify_keep(d, qjl, codebook):
     dec = tq.tq_decode_attention(cb, cache, qr[:, 0].contiguous()).cpu().double()
     assert ((dec - ref[:, 0]).abs().amax(-1) <= 2e-3 * ref[:, 0].abs().amax(-1) + tol[:, 0].amax(-1)).all()
     assert int(cache.status.item()) == 0
+
+
+def test_offsets_past_32_bits():
+    """A row whose codes pass 4 GB: drafts are appended at its end, attended, and
+    thinned.  The context's keys and values are zeros, so each of its tokens weighs
+    exp(0) and adds nothing."""
+    d, ctx, n = 256, 34_000_000, 5
+    cb = tq.Codebook(d, 4, 4)
+    cache = tq.Cache(cb, 1, 1, ctx + 16)
+    assert cache.k_codes.numel() > 1 << 32
+    cache.seq_lens.fill_(ctx)
+    rope = tq.Rope(d, 64)
+    x = torch.randn(1, n, 4, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda().transpose(1, 2)
+    x[:, 2:3] *= 3.0
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")[None].contiguous()
+    qr, _ = tq.tq_rope_append(cb, cache, rope, x[:, 2:3], x[:, 3:], q=x[:, :2], positions=pos)
+    out = tq.tq_tree_attention(cb, cache, qr).cpu().double()
+    # the drafts alone, as a row of their own: scores and values of the same bytes
+    small = tq.Cache(cb, 1, 1, 16)
+    for name in ("k_codes", "v_codes", "k_norm", "v_norm"):
+        getattr(small, name)[:, :, :n] = getattr(cache, name)[:, :, ctx:ctx + n]
+    small.seq_lens.fill_(n)
+    R = rotation(cb)
+    k, v = (decoded(cb, small, w, 0, 0, n) for w in "kv")
+    for h in range(2):
+        s = (qr[0, :, h].cpu().double() @ R.T) @ k.T / d ** 0.5
+        w = torch.where(torch.ones(n, n, dtype=torch.bool).tril(), s.exp(), torch.zeros_like(s))
+        want = (w @ v) @ R / (ctx + w.sum(-1, keepdim=True))
+        # the bound of tree_reference, on the weighted values; and half a bf16 step
+        u = 2.0 ** -11
+        delta = ((qr[0, :, h].cpu().double() @ R.T).abs() @ k.abs().T / d ** 0.5).amax(-1, keepdim=True)
+        tol = ((w @ v.abs()) * (3 * u + 4 * u * delta)).norm(dim=-1, keepdim=True) / ctx
+        assert ((out[0, :, h] - want).abs() <= tol + want.abs() * 2.0 ** -8).all()
+    kept = {name: getattr(cache, name)[:, :, [ctx, ctx + 3]].clone() for name in ("k_codes", "v_codes", "k_norm", "v_norm")}
+    tq.tq_cache_compact(cb, cache, torch.tensor([[0, 3]], dtype=torch.int32).cuda(), torch.tensor([2], dtype=torch.int32).cuda(),
+                        start=torch.tensor([ctx], dtype=torch.int32).cuda())
+    assert cache.seq_lens.tolist() == [ctx + 2] and int(cache.status.item()) == 0
+    for name, t in kept.items():
+        assert torch.equal(getattr(cache, name)[:, :, ctx:ctx + 2], t), name
+    # and a row copied from past 4 GB of the arrays
+    two = tq.Cache(cb, 2, 1, 17_000_016)
+    two.k_codes[1, 0, :48] = torch.arange(48, dtype=torch.uint8, device="cuda")[:, None]
+    two.seq_lens.copy_(torch.tensor([0, 17_000_001], dtype=torch.int32))
+    one = tq.Cache(cb, 1, 1, 17_000_016)
+    tq.tq_cache_copy(cb, one, two, torch.tensor([0], dtype=torch.int32).cuda(), torch.tensor([1], dtype=torch.int32).cuda())
+    assert one.seq_lens.tolist() == [17_000_001]
+    assert torch.equal(one.k_codes[0, 0, :64], two.k_codes[1, 0, :64])
+
+
+def test_a_stream_of_its_own_and_whole_rows():
+    """A call on a stream of its own orders what it allocates there; drafts rejected
+    whole (a count of zero) and accepted whole leave a row as it should be."""
+    cb = tq.Codebook(64, 2, 2)
+    cache = tq.Cache(cb, 2, 1, 64)
+    rope = tq.Rope(64, 64)
+    x = torch.randn(2, 4, 3, 64, generator=torch.Generator().manual_seed(3)).half().cuda().transpose(1, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for step in range(3):
+        qr, _ = tq.tq_rope_append(cb, cache, rope, x[:, 1:2], x[:, 2:], q=x[:, :1], stream=s)
+        out = tq.tq_tree_attention(cb, cache, qr, stream=s)
+        tq.tq_cache_compact(cb, cache, torch.arange(4, dtype=torch.int32).expand(2, 4).contiguous().cuda(),
+                            torch.tensor([4, 0], dtype=torch.int32).cuda(),
+                            start=torch.tensor([4 * step, 0], dtype=torch.int32).cuda(), stream=s)
+    s.synchronize()
+    assert cache.seq_lens.tolist() == [12, 0] and int(cache.status.item()) == 0
+    assert torch.isfinite(out).all()

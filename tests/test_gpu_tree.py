@@ -248,3 +248,25 @@ def test_many_rows():
     lens = [(b * 7) % 33 if b % 5 == 0 else 0 for b in range(B)]
     cache = fill_cache(tq, cb, B, 1, 48, lens, seed=1)
     _check(cb, cache, _q((B, n, 2, 64), torch.float16, 2), chain(n), lens, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows", [(6, 2), (50, 8)])
+def test_a_bad_query_stays_in_its_row(dtype, rows):
+    """Infinities and NaN in one draft's query; the scale that the rows share is the others'."""
+    n, G = rows
+    cb = tq.Codebook(128, 3, 4, qjl=True)
+    lens = [n + 100]
+    cache = fill_cache(tq, cb, 1, 1, 176, lens, seed=2)
+    q = _q((1, n, G, 128), dtype, 1)
+    q[0, 1, 0, 5], q[0, 2, 1, 9] = math.inf, math.nan
+    got = tq.tq_tree_attention(cb, cache, q.cuda())
+    ok = torch.ones(n, G, dtype=torch.bool)
+    ok[1, 0] = ok[2, 1] = False
+    assert not torch.isfinite(got[0].cpu()[~ok]).any()
+    clean = q.clone()
+    clean[0, 1, 0] = clean[0, 2, 1] = 0
+    ref, tol = tree_reference(cb, cache, clean, chain(n), lens)
+    got = got.cpu()
+    got[0][~ok], ref[0][~ok] = 0, 0
+    assert_tree_close(got, ref, tol)

@@ -387,6 +387,7 @@ cudaError_t launch_dim(const Tables& tb, const CacheView& cv, const TreeArgs& ta
   cfg.stream = stream;
   // shares of 32 rows, until there is a block for each SM
   const long units = pl.slots - pl.ctas;
+  if (units > 0x7fffffffL || (long)ta.n_q * ta.q_heads > 0x7fffffffL) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3((unsigned)units, (unsigned)std::max(1L, std::min((pl.rows + 31) / 32L, kTreeMaxCtas / units)));
   cfg.blockDim = dim3(kPrepThreads);
   cudaError_t e = cudaLaunchKernelEx(&cfg, tree_query_kernel<D>, tb, cv, ta, pl, ws);
