@@ -413,7 +413,7 @@ class _on:
 
     def __init__(self, device: torch.device, stream):
         self.entered, self.index = (), device.index
-        if stream is None and device.index == torch.cuda.current_device():
+        if stream is None and device.index == torch._C._cuda_getDevice():
             return
         self.entered = []
         if device.index != torch.cuda.current_device():
@@ -429,8 +429,9 @@ class _on:
         return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        for c in reversed(self.entered):
-            c.__exit__(*exc)
+        if self.entered:
+            for c in reversed(self.entered):
+                c.__exit__(*exc)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -454,24 +455,33 @@ def _index_ptr(where: str, name: str, t: torch.Tensor | None, shape: tuple, devi
 
 def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) -> tq_cache:
     """The cache's arrays, each as large as the codebook asks for, contiguous and on
-    the cache's device."""
+    the cache's device.  (Written out: it runs on every call.)"""
     if device.type != "cuda":
         _refuse_device(where, "cache", cache.seq_lens, device)
-    index, (kb, vb, meta, sb) = device.index, cb.slot_elements
+    i, (kb, vb, meta, sb) = device.index, cb.slot_elements
     b, h, c = cache.batch, cache.kv_heads, cache.capacity
     n = b * h * c
-    kc, vc, kn, vn, ks, kr = cache.k_codes, cache.v_codes, cache.k_norm, cache.v_norm, None, None
+    kc, vc, kn, vn = cache.k_codes, cache.v_codes, cache.k_norm, cache.v_norm
     sl, st, sy = cache.seq_lens, cache.status, cache.append_sync
-    want = ((kc, n * kb), (vc, n * vb), (kn, n * meta), (vn, n * meta), (sl, b), (st, 1), (sy, b))
-    if sb:
-        ks, kr = cache.k_signs, cache.k_rnorm
-        want += ((ks, n * sb), (kr, n))
-    for t, count in want:
-        if t is None or t.numel() != count or t.get_device() != index or not t.is_contiguous():
-            name = next(k for k, v in vars(cache).items() if v is t)
-            raise ValueError(f"{where}: cache.{name} must be a contiguous tensor of {count} elements on {device}")
-    return tq_cache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr() if sb else None, kn.data_ptr(), vn.data_ptr(),
-                    kr.data_ptr() if sb else None, sl.data_ptr(), st.data_ptr(), sy.data_ptr(), b, h, c)
+    try:
+        good = (kc.numel() == n * kb and vc.numel() == n * vb and kn.numel() == vn.numel() == n * meta and
+                sl.numel() == sy.numel() == b and st.numel() == 1 and
+                kc.get_device() == vc.get_device() == kn.get_device() == vn.get_device() == sl.get_device() ==
+                st.get_device() == sy.get_device() == i and
+                kc.is_contiguous() and vc.is_contiguous() and kn.is_contiguous() and vn.is_contiguous() and
+                sl.is_contiguous() and sy.is_contiguous())
+        ks = kr = None
+        if good and sb:
+            ks, kr = cache.k_signs, cache.k_rnorm
+            good = (ks.numel() == n * sb and kr.numel() == n and ks.get_device() == kr.get_device() == i and
+                    ks.is_contiguous() and kr.is_contiguous())
+            ks, kr = ks.data_ptr(), kr.data_ptr()
+    except AttributeError:   # an array is None
+        good = False
+    if not good:
+        raise ValueError(f"{where}: the cache's arrays must be contiguous tensors of the codebook's sizes on {device}")
+    return tq_cache(kc.data_ptr(), vc.data_ptr(), ks, kn.data_ptr(), vn.data_ptr(), kr, sl.data_ptr(),
+                    st.data_ptr(), sy.data_ptr(), b, h, c)
 
 
 class Rope:
