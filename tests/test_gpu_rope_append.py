@@ -84,6 +84,13 @@ CASES = [  # d, kb, vb, qjl, codebook, rot, interleaved, dtype, B, Hq, H, n, lay
     (256, 2, 3, True, "affine", 10, True, torch.float32, 1, 2, 2, 1700, "fused"),
     (128, 2, 2, False, "gaussian", 2, False, torch.bfloat16, 2, 16, 8, 400, "heads"),
     (128, 3, 3, True, "gaussian", 8, True, torch.float32, 5, 1, 1, 1100, "fused"),
+    # bulk queries whose rotated channels are whole blocks of 16
+    (128, 3, 4, False, "gaussian", 64, True, torch.bfloat16, 2, 12, 2, 517, "fused"),
+    (128, 3, 4, False, "gaussian", 16, False, torch.float16, 1, 3, 1, 1501, "heads"),
+    (64, 2, 3, False, "gaussian", 64, True, torch.float32, 3, 5, 1, 701, "fused"),
+    (64, 2, 2, True, "affine", 48, False, torch.bfloat16, 1, 1, 1, 2049, "heads"),
+    (256, 4, 4, False, "gaussian", 256, False, torch.float16, 1, 8, 1, 600, "fused"),
+    (256, 2, 2, True, "gaussian", 160, True, torch.float32, 2, 2, 2, 900, "heads"),
 ]
 
 

@@ -78,6 +78,21 @@ __device__ __forceinline__ void rotate(float (&x)[E], const T* vec, const float2
                                        int rot, bool interleaved) {
   if (c0 >= rot) return;
   if (interleaved) {
+    if constexpr (E >= 4) {
+      if (c0 + E <= rot && (rot & 3) == 0) {  // whole block, 16-byte aligned entries: two at a time
+        const float4* t4 = reinterpret_cast<const float4*>(cs + c0 / 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 t = __ldg(t4 + e / 4);
+          const float a = x[e], b = x[e + 1], c = x[e + 2], d = x[e + 3];
+          x[e] = __fsub_rn(__fmul_rn(a, t.x), __fmul_rn(b, t.y));
+          x[e + 1] = __fadd_rn(__fmul_rn(b, t.x), __fmul_rn(a, t.y));
+          x[e + 2] = __fsub_rn(__fmul_rn(c, t.z), __fmul_rn(d, t.w));
+          x[e + 3] = __fadd_rn(__fmul_rn(d, t.z), __fmul_rn(c, t.w));
+        }
+        return;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < E; e += 2)
       if (c0 + e < rot) {
@@ -95,10 +110,12 @@ __device__ __forceinline__ void rotate(float (&x)[E], const T* vec, const float2
     float p[E];
     load_elems<E>(vec + (first ? c0 + half : c0 - half), p);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 f = __ldg(t + e);
-      const float own = __fmul_rn(x[e], f.x), other = __fmul_rn(p[e], f.y);
-      x[e] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
+    for (int e = 0; e < E; e += 2) {  // (half is even here, so pairs of entries are 16-byte aligned)
+      const float4 f = __ldg(reinterpret_cast<const float4*>(t + e));
+      const float own0 = __fmul_rn(x[e], f.x), other0 = __fmul_rn(p[e], f.y);
+      const float own1 = __fmul_rn(x[e + 1], f.z), other1 = __fmul_rn(p[e + 1], f.w);
+      x[e] = first ? __fsub_rn(own0, other0) : __fadd_rn(own0, other0);
+      x[e + 1] = first ? __fsub_rn(own1, other1) : __fadd_rn(own1, other1);
     }
   } else {
 #pragma unroll
@@ -204,6 +221,67 @@ __global__ void __launch_bounds__(kRopeThreads)
   if constexpr (BULK) pdl_trigger();
 }
 
+// Bulk queries, rot_dim a multiple of 16: a thread turns 8 pairs, both channels of
+// each, for every hs-th head of a token, so that a table entry is read once for all of
+// them: 8192 tokens of 32 heads in 29 us (4.6 TB/s), 55 us with one read per channel
+// and head.  Lanes past the rotated channels copy 16 channels.  Grid: (blocks of
+// tokens, batch).
+template <int D, typename T>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_query_kernel(const __grid_constant__ CacheView cv, const __grid_constant__ RopeAppend ra, int hs) {
+  constexpr int GL = D / 16, SLOTS = kRopeThreads / GL;
+  const int g = threadIdx.x % GL, slot = threadIdx.x / GL, b = blockIdx.y;
+  const int j = blockIdx.x * (SLOTS / hs) + slot / hs;
+  pdl_wait();
+  const int base = ra.start ? ra.start[b] : cv.seq_lens[b];
+  if (j < ra.n_new) {
+    const int half = ra.rot_dim >> 1;
+    const bool turns = 8 * g < half;
+    // channels of the thread's first and second eight
+    const int c0 = !turns ? ra.rot_dim + 16 * (g - half / 8) : ra.interleaved ? 16 * g : 8 * g;
+    const int c1 = turns && !ra.interleaved ? c0 + half : c0 + 8;
+    float4 t[4];
+    if (turns) {
+      long pos = ra.positions ? ra.positions[(long)b * ra.n_new + j] : j;
+      if (!ra.positions || ra.relative) pos += base;
+      const long at = min(max(pos, 0l), (long)ra.max_pos - 1);
+      if (at != pos && g == 0) atomicOr(cv.status, (int)kFlagIndex);
+      const float4* cs = reinterpret_cast<const float4*>(reinterpret_cast<const float2*>(ra.table) + at * half + 8 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = __ldg(cs + i);
+    }
+    const T* src = static_cast<const T*>(ra.q.data) + b * ra.q.sb + j * ra.q.st;
+    T* dst = static_cast<T*>(ra.q_out) + ((long)b * ra.n_new + j) * ra.q_heads * D;
+#pragma unroll 4
+    for (int h = slot % hs; h < ra.q_heads; h += hs) {
+      float x[8], y[8];
+      load_elems<8>(src + h * ra.q.sh + c0, x);
+      load_elems<8>(src + h * ra.q.sh + c1, y);
+      if (turns) {
+        auto turn = [](float& a, float& b, float c, float s) {
+          const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+          b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+          a = u;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (ra.interleaved) {
+            float(&z)[8] = i < 2 ? x : y;
+            turn(z[4 * (i & 1)], z[4 * (i & 1) + 1], t[i].x, t[i].y);
+            turn(z[4 * (i & 1) + 2], z[4 * (i & 1) + 3], t[i].z, t[i].w);
+          } else {
+            turn(x[2 * i], y[2 * i], t[i].x, t[i].y);
+            turn(x[2 * i + 1], y[2 * i + 1], t[i].z, t[i].w);
+          }
+        }
+      }
+      store_elems<8>(dst + h * D + c0, x);
+      store_elems<8>(dst + h * D + c1, y);
+    }
+  }
+  pdl_trigger();
+}
+
 // At most this many vectors in all take the layout of one vector per warp, as
 // the append does: too few to fill the GPU, so latency rules.
 constexpr long kRopeLatencyVectors = 4096;
@@ -240,7 +318,22 @@ cudaError_t launch_typed(const Tables& tb, const CacheView& cv, const RopeAppend
   // bulk: a grid per kind, each of one code width (its unrolled encoder stays in
   // the instruction cache); the last one publishes the lengths
   cudaError_t e = cudaSuccess;
-  if (ra.q.data) {
+  if (ra.q.data && ra.rot_dim % 16 == 0) {
+    const int hs = ra.q_heads >= 8 ? 8 : ra.q_heads >= 4 ? 4 : ra.q_heads >= 2 ? 2 : 1;
+    const int tokens = kRopeThreads / (D / 16) / hs;
+    const long nb = ((long)ra.n_new + tokens - 1) / tokens;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nb, (unsigned)cv.batch);
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, rope_query_kernel<D, T>, cv, ra, hs);
+    if (e != cudaSuccess) return e;
+  } else if (ra.q.data) {
     constexpr int E = 8;
     e = launch(rope_append_kernel<D, T, E, false, kQueries, 2, true>, blocks(D / E, ra.q_heads), cv.batch,
                stream, tb, cv, ra, 0, 0);
