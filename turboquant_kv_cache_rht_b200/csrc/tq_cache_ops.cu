@@ -50,61 +50,80 @@ __device__ __forceinline__ void publish_row(const CacheView& cv, int b, int bloc
   }
 }
 
-constexpr int kCompactThreads = 512, kCompactPer = 4;
+constexpr int kCompactThreads = 1024, kCompactPer = 4;
 
-// Moves a column's kept entries down, in order.  Entry i comes from slot
-// index[i] >= i, so a chunk's stores only touch slots that this chunk or an
-// earlier one has read: they follow the barrier after its loads, while the next
-// chunk's loads (from slots past these stores) and the indices of the one after
-// are already under way: a chunk costs one memory latency.
-template <typename W>
-__device__ __forceinline__ bool move_column(uint8_t* col, int slot_bytes, const int32_t* __restrict__ idx, int count,
-                                            int limit, bool checks) {
-  constexpr int CHUNK = kCompactThreads * kCompactPer;
+// Moves kept entries down, in order: load(slot) gives an entry's bytes, store(slot,
+// bytes) writes them.  Entry i comes from slot index[i] >= i, so a chunk's stores only
+// touch slots that this chunk or an earlier one has read: they follow the barrier
+// after its loads, while the next chunk's loads (from slots past these stores) and the
+// indices of the one after are already under way: a chunk costs one memory latency.
+// CHECKS: the list's order too (one block of a (row, head) does).
+template <typename W, bool CHECKS, typename Load, typename Store>
+__device__ __forceinline__ bool move_entries(const int32_t* __restrict__ idx, int count, int limit, Load load,
+                                             Store store) {
+  constexpr int CHUNK = kCompactThreads * kCompactPer, NP = CHECKS ? kCompactPer : 1;
   const int tid = threadIdx.x;
   bool good = true;
-  auto indices = [&](int c0, int (&s)[kCompactPer], int (&before)[kCompactPer]) {
+  auto indices = [&](int c0, int (&s)[kCompactPer], int (&before)[NP]) {
 #pragma unroll
     for (int j = 0; j < kCompactPer; ++j) {
       const int i = c0 + j * kCompactThreads + tid;
       s[j] = i < count ? idx[i] : INT_MAX;  // (past the list: not a slot)
-      before[j] = checks && i < count && i > 0 ? idx[i - 1] : -1;
+      if constexpr (CHECKS) before[j] = i < count && i > 0 ? idx[i - 1] : -1;
     }
   };
-  auto loads = [&](int c0, const int (&s)[kCompactPer], const int (&before)[kCompactPer], W (&v)[kCompactPer]) {
+  auto loads = [&](int c0, const int (&s)[kCompactPer], const int (&before)[NP], W (&v)[kCompactPer]) {
 #pragma unroll
     for (int j = 0; j < kCompactPer; ++j) {
       const bool in = s[j] >= 0 && s[j] < limit;
-      if (c0 + j * kCompactThreads + tid < count) good = good && in && s[j] > before[j];
-      if (in) v[j] = *reinterpret_cast<const W*>(col + (long)s[j] * slot_bytes);
+      if (c0 + j * kCompactThreads + tid < count) {
+        good = good && in;
+        if constexpr (CHECKS) good = good && s[j] > before[j];
+      }
+      if (in) v[j] = load(s[j]);
     }
   };
-  int s0[kCompactPer], s1[kCompactPer], p0[kCompactPer], p1[kCompactPer];
+  int s0[kCompactPer], s1[kCompactPer], p0[NP], p1[NP];
   W v0[kCompactPer], v1[kCompactPer];
   indices(0, s0, p0);
   indices(CHUNK, s1, p1);
   loads(0, s0, p0, v0);
   for (int c0 = 0; c0 < count; c0 += CHUNK) {
     loads(c0 + CHUNK, s1, p1, v1);
-    int s2[kCompactPer], p2[kCompactPer];
+    int s2[kCompactPer], p2[NP];
     indices(c0 + 2 * CHUNK, s2, p2);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kCompactPer; ++j) {
-      if (s0[j] >= 0 && s0[j] < limit)
-        *reinterpret_cast<W*>(col + (long)(c0 + j * kCompactThreads + tid) * slot_bytes) = v0[j];
+      if (s0[j] >= 0 && s0[j] < limit) store(c0 + j * kCompactThreads + tid, v0[j]);
       s0[j] = s1[j];
       s1[j] = s2[j];
-      p1[j] = p2[j];
+      if constexpr (CHECKS) p1[j] = p2[j];
       v0[j] = v1[j];
     }
   }
   return good;
 }
 
-// Grid: (columns, kv_heads, batch).
-__global__ void __launch_bounds__(kCompactThreads, 2)
-    compact_kernel(const __grid_constant__ Columns cols, const __grid_constant__ CacheView cv,
+template <typename W>
+__device__ __forceinline__ bool move_column(uint8_t* col, int slot_bytes, const int32_t* idx, int count, int limit,
+                                            bool checks) {
+  auto load = [&](int s) { return *reinterpret_cast<const W*>(col + (long)s * slot_bytes); };
+  auto store = [&](int i, const W& x) { *reinterpret_cast<W*>(col + (long)i * slot_bytes) = x; };
+  return checks ? move_entries<W, true>(idx, count, limit, load, store)
+                : move_entries<W, false>(idx, count, limit, load, store);
+}
+
+// The 2-byte columns of a row together (norms): up to three.
+struct Halves {
+  uint16_t x[3];
+};
+
+// Grid: (the 2-byte columns as one, if there are any, then the others; kv_heads;
+// batch).  (A block for each 2-byte column took as long as one of 16 bytes, and made
+// more blocks than the SMs hold.)
+__global__ void __launch_bounds__(kCompactThreads, 1)
+    compact_kernel(const __grid_constant__ Columns cols, const __grid_constant__ CacheView cv, int halves,
                    const int32_t* __restrict__ index, long stride_b, long stride_h,
                    const int32_t* __restrict__ counts, int max_count, const int32_t* __restrict__ start) {
   const int h = blockIdx.y, b = blockIdx.z;
@@ -112,14 +131,33 @@ __global__ void __launch_bounds__(kCompactThreads, 2)
   const RowPlan r = plan_row(cv, b, counts, max_count, start);
   bool good = r.sound;
   if (r.sound) {
-    const Column& c = cols.c[blockIdx.x];
-    uint8_t* col = c.base + (((long)b * cv.kv_heads + h) * cv.capacity + r.first) * c.slot_bytes + c.offset;
     const int32_t* idx = index + b * stride_b + h * stride_h;
-    const bool checks = blockIdx.x == 0;  // the list's order, once
-    if (c.width == 16) good = move_column<uint4>(col, c.slot_bytes, idx, r.count, r.room, checks);
-    else if (c.width == 8) good = move_column<uint2>(col, c.slot_bytes, idx, r.count, r.room, checks);
-    else if (c.width == 4) good = move_column<uint32_t>(col, c.slot_bytes, idx, r.count, r.room, checks);
-    else good = move_column<uint16_t>(col, c.slot_bytes, idx, r.count, r.room, checks);
+    const long slot0 = ((long)b * cv.kv_heads + h) * cv.capacity + r.first;
+    if (halves > 0 && blockIdx.x == 0) {
+      uint16_t* col[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) col[k] = reinterpret_cast<uint16_t*>(cols.c[k < halves ? k : 0].base) + slot0;
+      good = move_entries<Halves, true>(
+          idx, r.count, r.room,
+          [&](int s) {
+            Halves x;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) x.x[k] = k < halves ? col[k][s] : (uint16_t)0;
+            return x;
+          },
+          [&](int i, const Halves& x) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              if (k < halves) col[k][i] = x.x[k];
+          });
+    } else {
+      const Column& c = cols.c[blockIdx.x + (halves > 0 ? halves - 1 : 0)];
+      uint8_t* col = c.base + slot0 * c.slot_bytes + c.offset;
+      const bool checks = blockIdx.x == 0;
+      if (c.width == 16) good = move_column<uint4>(col, c.slot_bytes, idx, r.count, r.room, checks);
+      else if (c.width == 8) good = move_column<uint2>(col, c.slot_bytes, idx, r.count, r.room, checks);
+      else good = move_column<uint32_t>(col, c.slot_bytes, idx, r.count, r.room, checks);
+    }
   }
   publish_row(cv, b, gridDim.x * gridDim.y, r.first + r.count, good);
   pdl_trigger();
@@ -261,19 +299,24 @@ cudaError_t launch(Kernel kern, dim3 grid, int threads, cudaStream_t stream, Arg
 cudaError_t launch_cache_compact(const SlotArrays& arrays, const CacheView& cv, const int32_t* index,
                                  long stride_b, long stride_h, const int32_t* counts, int max_count,
                                  const int32_t* start, cudaStream_t stream) {
-  Columns cols = {};
-  for (int a = 0; a < arrays.n; ++a) {
-    const int bytes = arrays.bytes[a];
-    const int width = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : bytes % 4 == 0 ? 4 : 2;
-    for (int o = 0; o < bytes; o += width) cols.c[cols.n++] = Column{arrays.p[a], bytes, o, width};
-  }
+  Columns cols = {};  // the 2-byte ones first
+  int halves = 0;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int a = 0; a < arrays.n; ++a) {
+      const int bytes = arrays.bytes[a];
+      const int width = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : bytes % 4 == 0 ? 4 : 2;
+      if ((width == 2) != (pass == 0)) continue;
+      for (int o = 0; o < bytes; o += width) cols.c[cols.n++] = Column{arrays.p[a], bytes, o, width};
+      halves += width == 2 ? 1 : 0;  // (an array of 2-byte slots: norms)
+    }
   // A list whose pieces one block holds at once takes a block per (row, head): 64
   // drafts of 32 rows and 8 heads cut to 6 in 4 us instead of the 10 that a block
   // per column takes to start and to meet; long lists need the columns' blocks.
   if ((long)max_count * cols.n <= kSmallThreads * kSmallPer)
     return launch(compact_small_kernel, dim3(1, cv.kv_heads, cv.batch), kSmallThreads, stream, cols, cv, index,
                   stride_b, stride_h, counts, max_count, start);
-  return launch(compact_kernel, dim3(cols.n, cv.kv_heads, cv.batch), kCompactThreads, stream, cols, cv, index,
+  const int blocks = cols.n - (halves > 0 ? halves - 1 : 0);
+  return launch(compact_kernel, dim3(blocks, cv.kv_heads, cv.batch), kCompactThreads, stream, cols, cv, halves, index,
                 stride_b, stride_h, counts, max_count, start);
 }
 
