@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
 #pragma unroll 1
       for (int it = 0; it < sg.tiles; ++it) {
         const int slot = (n_tiles + it) % kMetaSlots, tok0 = sg.t0 + it * kTile + 32 * w + g;
-        const bool masked = sg.t0 + (it + 1) * kTile > ctx;
+        // (past a row's end as past its context: max_ctx may cut the row inside it)
+        const bool masked = sg.t0 + (it + 1) * kTile > min(ctx, sg.len);
         float kn[4], vn[4], ev[4];
 #pragma unroll
         for (int chunk = 0; chunk < CPT; ++chunk) {
