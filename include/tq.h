@@ -412,7 +412,8 @@ size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, in
  *        (0: one mask for every row).  NULL: a chain, j <= i.
  * out  : DEVICE `dtype`, like q.
  * The products' operands are fp16, their sums, the scores, maxima and sums fp32: the
- * weights are rounded to fp16, and so are the rotated queries of a bf16 call (an
+ * weights are rounded to fp16 (one below 2^-29 of a row's largest may be lost, so 128k
+ * such tokens cost 2^-12 of the row at most), and so are the rotated queries of a bf16 call (an
  * fp16 call holds them in two parts, 22 bits) and the affine codec's keys and values.
  * A draft that attends nothing gives zeros, as do all drafts of a row that holds
  * fewer than n_q tokens.  What a draft does not attend never reaches it, whatever

@@ -54,11 +54,15 @@ constexpr int kTreeMaxCtas = 148;   // one block per SM; the workspace is sized 
 // warps that had finished tile t - 5 or a later one: six slots need no barrier.
 constexpr int kMetaSlots = 6;
 constexpr int kMaxStages = 8;
-// Slack of the running maximum (log2): weights stay below 2^14, fp16 holds 2^16,
-// and 2^-14 of the largest is still a normal number.  A key that resembles the
-// query outscores the others by about 2^13 at head_dim 128, so that a slack of 8
-// raised the maximum of some column in most tiles (4x the time of the softmax).
-constexpr float kTreeLazyLog2 = 14.0f;
+// The running maximum (log2), of score + log2 |v|, moves when a weight passes 2^15.9
+// (fp16 holds 2^16) and then brings the largest to 2^4.  Above: a key that resembles the
+// query outscores the others by about 2^13 at head_dim 128, so that little room would
+// raise the maximum of some column in most tiles.  Below: a weight under 2^-25 is lost,
+// and a long flat tail's weights are small but many: 2^-29 of the largest for each token,
+// 2^-12 for 128k of them.  63 drafts at 32k, 16 ragged rows, 4 x 128k with the sketch:
+// 78, 197, 437 us; bringing it to 1 instead (2^-25, 0.4 % of such a row) 76, 194, 417 us;
+// to 2^7 86, 212, 522 us.
+constexpr float kTreeLazyLog2 = 15.9f, kTreeRaiseLog2 = 4.0f;
 constexpr float kNoMax = -1e30f;    // running maximum before any score (finite: no inf - inf)
 
 // Bytes of the tables: 2-bit codes four at a time (8 bytes, 16 copies), 3-bit
@@ -287,8 +291,8 @@ __device__ __forceinline__ bool raise_max(const Raise& a, const float (&kn)[4], 
   if (w == 0 && lane < 8 * NJ) {
     const uint32_t at = a.a_m + 4 * lane, red = a.sm_red + 4 * lane;
     const float old = -tm::ldsf(at);
-    const float mn = fmaxf(fmaxf(fmaxf(old, tm::ldsf(red)), tm::ldsf(red + 256)),
-                           fmaxf(tm::ldsf(red + 512), tm::ldsf(red + 768)));
+    const float mn = fmaxf(old, fmaxf(fmaxf(tm::ldsf(red), tm::ldsf(red + 256)),
+                                      fmaxf(tm::ldsf(red + 512), tm::ldsf(red + 768))) - kTreeRaiseLog2);
     tm::stsf(at, -mn);
     tm::stsf(a.sm_al + 4 * lane, fast_exp2(old - mn));
   }
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
             vis = visible<NJ>(tok0, sg.len, ctx, row0 + chunk * CN + part + 2 * qd, live_rows, ta.log_group, mask,
                               words);
           // The running maximum (of score + log2 |v|, so that every weight p |v| stays
-          // below 2^14 whatever the norms) moves only when a score passes it by that: in
+          // an fp16 number whatever the norms) moves only when a score passes it by that: in
           // a unit's first tile, afterwards almost never, and all four warps vote together.
           for (bool raise = it == 0;;) {
             if (__builtin_expect(raise, 0)) {
