@@ -681,3 +681,8 @@ def tq_cache_copy(cb: Codebook, dst: Cache, src: Cache, dst_rows: torch.Tensor, 
     with _on(dev, stream) as s:
         _check(lib.tq_cache_copy(cb.handle, cd, cs, to, come, lens, n, src.capacity if max_len is None else max_len, s),
                where)
+
+
+def tq_free(cb: Codebook) -> None:
+    """Release a codebook's handle before the object's own end; it cannot be used afterwards."""
+    cb.__del__()
