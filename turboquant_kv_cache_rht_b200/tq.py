@@ -454,8 +454,8 @@ def _index_ptr(where: str, name: str, t: torch.Tensor | None, shape: tuple, devi
 
 
 def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) -> tq_cache:
-    """The cache's arrays, each as large as the codebook asks for, contiguous and on
-    the cache's device.  (Written out: it runs on every call.)"""
+    """The cache's arrays, each of its type, as large as the codebook asks for,
+    contiguous and on the cache's device.  (Written out: it runs on every call.)"""
     if device.type != "cuda":
         _refuse_device(where, "cache", cache.seq_lens, device)
     i, (kb, vb, meta, sb) = device.index, cb.slot_elements
@@ -466,6 +466,8 @@ def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) 
     try:
         good = (kc.numel() == n * kb and vc.numel() == n * vb and kn.numel() == vn.numel() == n * meta and
                 sl.numel() == sy.numel() == b and st.numel() == 1 and
+                kc.dtype is vc.dtype is torch.uint8 and kn.dtype is vn.dtype is torch.float16 and
+                sl.dtype is sy.dtype is st.dtype is torch.int32 and
                 kc.get_device() == vc.get_device() == kn.get_device() == vn.get_device() == sl.get_device() ==
                 st.get_device() == sy.get_device() == i and
                 kc.is_contiguous() and vc.is_contiguous() and kn.is_contiguous() and vn.is_contiguous() and
@@ -473,13 +475,15 @@ def _cache_struct(where: str, cb: Codebook, cache: Cache, device: torch.device) 
         ks = kr = None
         if good and sb:
             ks, kr = cache.k_signs, cache.k_rnorm
-            good = (ks.numel() == n * sb and kr.numel() == n and ks.get_device() == kr.get_device() == i and
+            good = (ks.numel() == n * sb and kr.numel() == n and ks.dtype is torch.uint8 and
+                    kr.dtype is torch.float16 and ks.get_device() == kr.get_device() == i and
                     ks.is_contiguous() and kr.is_contiguous())
             ks, kr = ks.data_ptr(), kr.data_ptr()
     except AttributeError:   # an array is None
         good = False
     if not good:
-        raise ValueError(f"{where}: the cache's arrays must be contiguous tensors of the codebook's sizes on {device}")
+        raise ValueError(f"{where}: the cache's arrays must be contiguous tensors of the codebook's sizes and "
+                         f"types on {device}")
     return tq_cache(kc.data_ptr(), vc.data_ptr(), ks, kn.data_ptr(), vn.data_ptr(), kr, sl.data_ptr(),
                     st.data_ptr(), sy.data_ptr(), b, h, c)
 
