@@ -734,10 +734,13 @@ tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const 
                 "(group must be 1, 2, 4 or 8; v_bits must be k_bits or k_bits + 1)",
                 d, group, cb->params.k_bits, cb->params.v_bits, cb->params.qjl);
   const size_t need = tq::tree_workspace_bytes(cb->tables, cache->batch, q_heads, cache->kv_heads, n_q, max_ctx);
-  if (need > 0 && (!workspace || workspace_bytes < need))
+  if (need == 0)
+    return fail(TQ_ERR_UNSUPPORTED, "no tree attention for head_dim=%d k_bits=%d v_bits=%d qjl=%d: its buffers do not fit",
+                d, cb->params.k_bits, cb->params.v_bits, cb->params.qjl);
+  if (!workspace || workspace_bytes < need)
     return fail(TQ_ERR_CAPACITY, "workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, need);
-  if (need > 0 && !aligned16(workspace)) return fail(TQ_ERR_INVALID, "workspace must be 16-byte aligned");
+  if (!aligned16(workspace)) return fail(TQ_ERR_INVALID, "workspace must be 16-byte aligned");
   tq::TreeArgs ta;
   ta.q = q;
   ta.out = out;
