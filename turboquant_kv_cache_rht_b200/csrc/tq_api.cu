@@ -382,6 +382,7 @@ tq::SlotArrays arrays_of(const tq_codebook* cb, const tq_cache* c) {
 
 tq_status cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();
+  if (e == cudaErrorNotSupported) return fail(TQ_ERR_UNSUPPORTED, "%s: no kernel for this shape on this device", what);
   return fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

@@ -277,16 +277,21 @@ cudaError_t launch_dim(const Tables& tb, const CacheView& cv, const TreeArgs& ta
   // shares of 32 rows, until there is a block for each SM
   const long units = pl.slots - pl.ctas;
   if (units > 0x7fffffffL || (long)ta.n_q * ta.q_heads > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+  auto tree = [&](cudaLaunchConfig_t* c) {
+    return tb.affine ? (tb.qjl ? launch_tree_dim<D, true, true>(tb, cv, ta, pl, ws, c)
+                               : launch_tree_dim<D, true, false>(tb, cv, ta, pl, ws, c))
+                     : (tb.qjl ? launch_tree_dim<D, false, true>(tb, cv, ta, pl, ws, c)
+                               : launch_tree_dim<D, false, false>(tb, cv, ta, pl, ws, c));
+  };
+  cudaError_t e = tree(nullptr);  // nothing is launched unless all can be
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)units, (unsigned)std::max(1L, std::min((pl.rows + 31) / 32L, kTreeMaxCtas / units)));
   cfg.blockDim = dim3(kPrepThreads);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_query_kernel<D>, tb, cv, ta, pl, ws);
+  e = cudaLaunchKernelEx(&cfg, tree_query_kernel<D>, tb, cv, ta, pl, ws);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(pl.ctas);
   cfg.dynamicSmemBytes = pl.smem;
-  e = tb.affine ? (tb.qjl ? launch_tree_dim<D, true, true>(tb, cv, ta, pl, ws, &cfg)
-                          : launch_tree_dim<D, true, false>(tb, cv, ta, pl, ws, &cfg))
-                : (tb.qjl ? launch_tree_dim<D, false, true>(tb, cv, ta, pl, ws, &cfg)
-                          : launch_tree_dim<D, false, false>(tb, cv, ta, pl, ws, &cfg));
+  e = tree(&cfg);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(ta.n_q * ta.q_heads), (unsigned)cv.batch);
   cfg.blockDim = dim3(32 * kMergeWarps);

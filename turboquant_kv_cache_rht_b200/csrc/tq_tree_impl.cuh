@@ -45,6 +45,8 @@
 #include "tq_decode_impl.cuh"
 #include "tq_tmem.cuh"
 
+#include <atomic>
+
 namespace tq {
 
 constexpr int kTile = 128;          // tokens per tile: the matrix instruction's rows
@@ -914,16 +916,40 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
   }
 }
 
+// Whether a kernel's dynamic shared memory starts at kDynSmemBase on the current device
+// (no static shared memory, that much reserved per block), as its plans assume.  Asked
+// once per device: `known` holds a bit for each that is sound.
+template <typename Kernel>
+cudaError_t check_smem_base(Kernel kern, std::atomic<uint64_t>& known) {
+  int dev = 0, reserved = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= KernelConfig::kMaxDevices) return cudaErrorInvalidDevice;
+  if ((known.load(std::memory_order_relaxed) >> dev) & 1u) return cudaSuccess;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+  if (e != cudaSuccess) return e;
+  if (fa.sharedSizeBytes != 0 || reserved != (int)kDynSmemBase) return cudaErrorNotSupported;
+  known.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 
-// Launches the kernel of one compile-time shape (the rest of *cfg is set).
+// Launches the kernel of one compile-time shape (the rest of *cfg is set); without cfg,
+// only makes sure that it can be launched.
 template <int D, int CN, int CPT, int KB, int VB, bool QJL, bool AFF>
 cudaError_t launch_tree_shape(const Tables& tb, const CacheView& cv, const TreeArgs& ta, const TreePlan& pl, uint8_t* ws,
                               cudaLaunchConfig_t* cfg) {
   static KernelConfig config;
+  static std::atomic<uint64_t> at_base{0};
+  static_assert(KernelConfig::kMaxDevices <= 64, "a bit per device");
   auto kern = tree_kernel<D, CN, CPT, KB, VB, QJL, AFF>;
-  // the attribute is set once per device, for the largest plan
-  cudaError_t e = configure_kernel(config, kern, 227 * 1024, Roles<D, CN>::THREADS, nullptr);
+  cudaError_t e = check_smem_base(kern, at_base);
   if (e != cudaSuccess) return e;
+  // the attribute is set once per device, for the largest plan
+  e = configure_kernel(config, kern, 227 * 1024, Roles<D, CN>::THREADS, nullptr);
+  if (e != cudaSuccess || !cfg) return e;
   cfg->blockDim = dim3(Roles<D, CN>::THREADS);
   return cudaLaunchKernelEx(cfg, kern, tb, cv, ta, pl, ws);
 }
