@@ -415,7 +415,8 @@ size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, in
  * weights are rounded to fp16 (one below 2^-29 of a row's largest may be lost, so 128k
  * such tokens cost 2^-12 of the row at most), and so are the rotated queries of a bf16 call (an
  * fp16 call holds them in two parts, 22 bits) and the affine codec's keys and values.
- * A draft that attends nothing gives zeros, as do all drafts of a row that holds
+ * Queries of one call may differ in size by any factor; a query that is not finite
+ * makes its own row NaN.  A draft that attends nothing gives zeros, as do all drafts of a row that holds
  * fewer than n_q tokens.  What a draft does not attend never reaches it, whatever
  * the cache holds there; a token whose value has no finite norm (or scale, or bias)
  * makes the drafts that attend it NaN.  softmax_scale, max_ctx, workspace: as for

@@ -61,7 +61,7 @@ static void check(const Tables& tb, int dtype, int n_q, int group) {
   CHECK(p.ctas >= 1 && p.ctas <= kTreeMaxCtas && p.slots == p.ctas + units && p.q_bytes == p.parts * p.rows * d * 2);
   CHECK(p.ws_ml >= p.slots * p.rows * d * 4 && p.ws_ml % 8 == 0 && p.ws_q >= p.ws_ml + p.slots * p.rows * 8);
   CHECK(p.ws_q % 128 == 0 && p.ws_scale >= p.ws_q + units * p.q_bytes && p.ws_scale % 4 == 0);
-  CHECK((long)plan_bytes(p) >= p.ws_scale + 4 * units);
+  CHECK(p.ws_rows >= p.ws_scale + 4 * units && p.ws_rows % 8 == 0 && (long)plan_bytes(p) >= p.ws_rows + units * p.rows * 4);
 }
 
 int main() {

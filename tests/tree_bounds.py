@@ -23,6 +23,10 @@ values v (in the output's frame), output o, rotated query x and keys k:
                  as a 2-norm, which the rotation back keeps
   small weights  a weight below 2^-14 is rounded to a multiple of 2^-24, where the
                  row's largest is at least 2^4: 2^-29 of it per token, at its worst
+  beyond         the above is of first order.  Where a score may be off by more than e =
+                 0.1, the output is still a mean of the values of tokens whose scores are
+                 within 2 e of the largest (others' weights, e^-28 or less, aside): it is
+                 off by no more than the farthest of these values is
 Elements are held to the sum of these, rows to their 2-norm, where the accumulation
 counts once.
 """
@@ -111,11 +115,13 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
                 sign = 2.0 * _codes(cache.k_signs[b, h, :end], 1).double() - 1.0
                 rn = torch.where(used[:, 0], cache.k_rnorm[b, h, :end].double(), zero) * math.sqrt(math.pi / (2 * d))
             unit = q[b, :, h * G:(h + 1) * G]
-            # below 2^-14 a query's half step is 2^-25, where |sqrt(d) x| <= d max|q| is brought to 2^14 (2^10)
-            floor = unit.abs().max() * math.sqrt(d) * 2.0 ** ((11 if not cb.qjl else 15) - 36)
+            # below 2^-14 a query's half step is 2^-25, where |sqrt(d) x| <= d max|q| is brought to
+            # 2^14 (2^10), by the unit's largest row or, where rows differ by 2^16, by its own
+            tiny = math.sqrt(d) * 2.0 ** ((11 if not cb.qjl else 15) - 36)
             for i in range(n):
                 for g in range(G):
                     x = R1 @ unit[i, g]
+                    floor = torch.minimum(unit.abs().max(), 2.0 ** 17 * unit[i, g].abs().max()) * tiny
                     sk = scale * rn * (sign @ (R2 @ x)) if cb.qjl else torch.zeros(end, dtype=torch.float64, device=dev)
 
                     def weights(keys):
@@ -136,7 +142,8 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
                     J = scale * (k * p[:, None]).T @ away
                     first = K * uq * (xx @ (J * J)).sqrt()
                     g2 = (k * k) @ xx * scale * scale
-                    worst = K * uq * g2[p > 1e-9].max().sqrt() if bool((p > 1e-9).any()) else zero
+                    any_seen = bool(vis[i].any())
+                    worst = K * uq * g2[vis[i]].max().sqrt() if any_seen else zero
                     if cb.qjl:
                         w = R2 @ x
                         J2 = scale * (sign * (rn * p)[:, None]).T @ away
@@ -149,9 +156,12 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
                         t = t + U * torch.minimum(K * ((p * p) @ vv).sqrt(), p @ vv.sqrt())
                         g2 = (k * k + 2.0 ** -28) @ xx * scale * scale
                         first = first + K * U * ((p * p * g2) @ (away * away)).sqrt()
-                        worst = worst + K * U * g2[p > 1e-9].max().sqrt() if bool((p > 1e-9).any()) else worst
+                        worst = worst + K * U * g2[vis[i]].max().sqrt() if any_seen else worst
                     lin = 2.0 ** -20 * (scale * (k.abs() @ x.abs()) + 2 * sk.abs() + 2 * torch.where(vis[i], s, zero).abs().max() + 4)
                     t = t + first * (1 + 2 * worst) + (p * lin) @ away.abs()
+                    e = worst + lin[vis[i]].max() if any_seen else zero
+                    if float(e) > 0.1:
+                        t = t + away[s >= s.max() - 2 * e - 28].abs().amax(0)
                     acc[b, i, h * G + g] = (end / 16 + 64) * 2.0 ** -23 * (p @ stored.abs()).norm()
                     small = (p * vn).max() * 2.0 ** -29
                     t = t + small * (v.abs() / vn.clamp_min(1e-300)[:, None]).masked_fill(~vis[i][:, None], 0.0).sum(0)

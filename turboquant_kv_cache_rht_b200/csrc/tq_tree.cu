@@ -13,15 +13,25 @@ namespace {
 // rows); every block reads all of the unit's rows for the scale (few units would
 // leave most SMs idle: one block per unit took 13 us for 8 units of 252 rows).  It
 // is common to its rows: |u| <= d max|q| is brought to 2^14, or 2^10 before the
-// second rotation, which can add sqrt(d).  Rows that are not finite do not count.
+// second rotation, which can add sqrt(d).  Rows that are not finite do not count, nor
+// do rows of zeros.  A unit's rows are wild
+//   where they differ by more than 2^16 (a padded draft with what its memory held): the
+//     small ones would lose bits under a common scale;
+//   where a score may pass 2^26 (the longest row with a key of the largest fp16 norm):
+//     score * norm - maximum, rounded once, and the maximum, rounded before, would differ
+//     by more than the weights have room for.
+// Then each row has a scale of its own, the unit's is 0, and the attention finishes every
+// score before it uses it (63 drafts at 32k: 138 us if wild, 79 if not).
 constexpr int kPrepThreads = 1024;
+constexpr int kWildLog2 = 16;
+constexpr float kWildScore = 0x1p26f;
 
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads)
     tree_query_kernel(const __grid_constant__ Tables tb, const __grid_constant__ CacheView cv,
                       const __grid_constant__ TreeArgs ta, const __grid_constant__ TreePlan pl, uint8_t* __restrict__ ws) {
-  constexpr int E = D / 32;
-  __shared__ float red[32];
+  constexpr int E = D / 32, kLogD = D == 64 ? 6 : D == 128 ? 7 : 8;
+  __shared__ uint32_t red[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c0 = lane * E;
   const int unit = blockIdx.x, units = cv.kv_heads * pl.blocks, b = unit / units, u0 = unit - b * units;
   const int kvh = u0 / pl.blocks, rb = u0 - kvh * pl.blocks, group = ta.q_heads / cv.kv_heads;
@@ -52,30 +62,43 @@ __global__ void __launch_bounds__(kPrepThreads)
       x[2 * e + 1] = f.y;
     }
   };
-  float amax = 0.f;
+  // max|x| of a row, as bits (whose order is that of floats that are not negative, then
+  // infinity, then NaN); 0 for one that does not count
+  auto size = [&](const float (&x)[E]) {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int e = 0; e < E; ++e) t = max(t, __float_as_uint(x[e]) & 0x7fffffffu);
+    t = __reduce_max_sync(0xffffffffu, t);
+    return t < 0x7f800000u ? t : 0u;
+  };
+  auto exponent = [&](uint32_t bits) {  // of d max|x|
+    int ex = 0;
+    frexpf(__uint_as_float(bits), &ex);
+    return bits ? ex + kLogD : 1;
+  };
+  auto scale_of = [&](int ex) { return ldexpf(1.f, max(min((tb.qjl ? 10 : 14) - ex, 100), -126)); };
+  uint32_t most = 0u, least = 0xffffffffu;
 #pragma unroll 4
   for (int rr = warp; rr < rows; rr += 32) {
-    float x[E], t = 0.f;
+    float x[E];
     load(rr, x);
-    bool finite = true;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      t = fmaxf(t, fabsf(x[e]));
-      finite = finite && fabsf(x[e]) < INFINITY;
-    }
-    if (__all_sync(0xffffffffu, finite)) amax = fmaxf(amax, t);
+    const uint32_t t = size(x);
+    most = max(most, t);
+    least = min(least, t - 1u);  // (0 becomes the largest)
   }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  if (lane == 0) red[warp] = amax;
+  if (lane == 0) {
+    red[0][warp] = most;
+    red[1][warp] = least;
+  }
   __syncthreads();
-  amax = red[lane];
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  int ex = 0;
-  frexpf(amax > 0.f ? amax * D : 1.f, &ex);
-  const float scale = ldexpf(1.f, max(min((tb.qjl ? 10 : 14) - ex, 100), -100));
-  if (tid == 0 && blockIdx.y == 0) reinterpret_cast<float*>(ws + pl.ws_scale)[unit] = scale;
+  most = __reduce_max_sync(0xffffffffu, red[0][lane]);
+  least = __reduce_min_sync(0xffffffffu, red[1][lane]);
+  const float root = sqrtf((float)D), longest = __uint_as_float(most) * root;
+  const float key = 65504.f * (tb.affine ? root : 1.f) * (tb.qjl ? 1.f + sqrtf(3.14159265358979f / 2.f) : 1.f);
+  const bool wild = (least < most && exponent(most) - exponent(least + 1u) > kWildLog2) ||
+                    longest * key * ta.scale * 1.4426950408889634f > kWildScore;
+  const float unit_scale = scale_of(exponent(most));
+  if (tid == 0 && blockIdx.y == 0) reinterpret_cast<float*>(ws + pl.ws_scale)[unit] = wild ? 0.f : unit_scale;
   uint8_t* table = ws + pl.ws_q + (long)unit * pl.q_bytes;
   const int blk = pl.rows * 128, part = pl.rows * D * 2;
 #pragma unroll 1
@@ -86,6 +109,11 @@ __global__ void __launch_bounds__(kPrepThreads)
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) u[e] = 0.f;
+    }
+    float scale = unit_scale;
+    if (wild) {
+      scale = scale_of(exponent(size(u)));
+      if (lane == 0) reinterpret_cast<float*>(ws + pl.ws_rows)[(long)unit * pl.rows + rr] = score_factor(tb, ta.scale) / scale;
     }
     auto signs = [&](const uint32_t* s, float by) {
       const uint32_t w = s[c0 >> 5] >> (c0 & 31);

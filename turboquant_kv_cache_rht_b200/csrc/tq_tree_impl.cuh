@@ -62,10 +62,17 @@ constexpr int kMaxStages = 8;
 // raise the maximum of some column in most tiles.  Below: a weight under 2^-25 is lost,
 // and a long flat tail's weights are small but many: 2^-29 of the largest for each token,
 // 2^-12 for 128k of them.  63 drafts at 32k, 16 ragged rows, 4 x 128k with the sketch:
-// 78, 197, 437 us; bringing it to 1 instead (2^-25, 0.4 % of such a row) 76, 194, 417 us;
+// 77, 195, 432 us; bringing it to 1 instead (2^-25, 0.4 % of such a row) 76, 194, 417 us;
 // to 2^7 86, 212, 522 us.
 constexpr float kTreeLazyLog2 = 15.9f, kTreeRaiseLog2 = 4.0f;
-constexpr float kNoMax = -1e30f;    // running maximum before any score (finite: no inf - inf)
+constexpr float kNoMax = -3e38f;    // running maximum before any score (finite: no inf - inf)
+
+// What a score is multiplied by after its product, beside its query's and its key's
+// scale: the softmax's scale, log2(e), and the 1/sqrt(d) of the rotation (and of the
+// dequantization).
+__device__ __forceinline__ float score_factor(const Tables& tb, float scale) {
+  return scale * 1.4426950408889634f / (tb.affine ? sqrtf((float)tb.d) : (float)tb.d * tb.k_lam);
+}
 
 // Bytes of the tables: 2-bit codes four at a time (8 bytes, 16 copies), 3-bit
 // pairs (32 copies), 4-bit pairs (16 copies: 32 would cost a stage).  A lane
@@ -82,7 +89,8 @@ struct TreePlan {
   int lut_k, lut_v, sm_q, sm_v, sm_p, sm_st, sm_meta, sm_misc, smem;  // shared addresses
   int st_v, st_s, st_kn, st_vn, st_rn, st_bytes;                      // inside a stage
   int ctas, q_bytes;       // q_bytes: one unit's query table
-  long slots, ws_ml, ws_q, ws_scale;  // workspace: bytes to the maxima and sums, query tables, their scales
+  // workspace: bytes to the maxima and sums, the query tables, their scales, the rows' factors
+  long slots, ws_ml, ws_q, ws_scale, ws_rows;
 };
 
 // Shared misc area: barriers, segments, then floats.
@@ -259,6 +267,21 @@ struct Raise {
   int wg, cols, blocks;                // blocks: 128-channel blocks of the output to rescale
 };
 
+// Multiplies a warp's scores in tensor memory, `cols` columns, by the columns' factors
+// and by the lane's token's norm.
+__device__ __forceinline__ void finish_scores(uint32_t at, int cols, const float* factors, float norm) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t x[16];
+    tm::ld_32x32b(at + c, x);
+    tm::wait_ld(x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factors[c + e] * norm);
+    tm::st_32x32b(at + c, x);
+  }
+  tm::wait_st();
+}
+
 // Raises the running maxima of NJ x 8 columns to the scores in tensor memory,
 // leaves the factors 2^(old - new) in sm_al and scales the outputs by them.
 // All four warps of the group call.  False: a wait gave up.
@@ -387,8 +410,7 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
     const int part = SUB * wg;  // first column of this warpgroup's in a chunk
     const uint32_t lanes = (uint32_t)(32 * w) << 16;
     const uint32_t sm_m = misc + kMiscM, sm_al = misc + kMiscAlpha + wg * 128, sm_red = misc + kMiscRed + wg * 1024;
-    // scores: folds softmax scale, log2(e) and the 1/sqrt(d) of the rotation (and of the dequantization)
-    const float post0 = ta.scale * 1.4426950408889634f / (AFF ? sqrtf((float)D) : (float)D * tb.k_lam);
+    const float post0 = score_factor(tb, ta.scale);
     const int live_rows = ta.n_q << ta.log_group, words = (ta.n_q + 31) >> 5;
     const int units = cv.kv_heads * pl.blocks;
     float l[CPT][2 * NJ];  // this thread's part of the sums
@@ -400,8 +422,10 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
       if (tm::bar_or(1 + wg, 128, !more)) break;  // all four warps leave together
       const long unit = (long)sg.b * units + sg.unit;
       const int row0 = (sg.unit % pl.blocks) * pl.rows;
-      // (the scale is a power of two: its division is exact)
-      const float post = post0 / reinterpret_cast<const float*>(ws + pl.ws_scale)[unit];
+      // (the scale is a power of two: its division is exact.  0 stands for a unit of wild
+      // rows, post < 0: its scores are finished one by one, in tensor memory)
+      const float q_scale = reinterpret_cast<const float*>(ws + pl.ws_scale)[unit];
+      const float post = q_scale == 0.f ? -1.f : post0 / q_scale;
       const int ctx = min(max(cv.seq_lens[sg.b], 0), cv.capacity) - ta.n_q;
       const uint32_t* mask = ta.mask ? ta.mask + sg.b * ta.mask_stride : nullptr;
       // column of the outputs (and maxima) of column i of this warpgroup's
@@ -416,8 +440,9 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
 #pragma unroll 1
       for (int it = 0; it < sg.tiles; ++it) {
         const int slot = (n_tiles + it) % kMetaSlots, tok0 = sg.t0 + it * kTile + 32 * w + g;
-        // (past a row's end as past its context: max_ctx may cut the row inside it)
-        const bool masked = sg.t0 + (it + 1) * kTile > min(ctx, sg.len);
+        // (past a row's end as past its context: max_ctx may cut the row inside it; a wild
+        // unit's tiles all take the masked ones' way)
+        const bool masked = sg.t0 + (it + 1) * kTile > (post < 0.f ? 0 : min(ctx, sg.len));
         float kn[4], vn[4], ev[4];
 #pragma unroll
         for (int chunk = 0; chunk < CPT; ++chunk) {
@@ -436,9 +461,16 @@ __global__ void __launch_bounds__(Roles<D, CN>::THREADS, 1)
           }
           float y[8 * NJ];
           uint32_t vis = 0xffffffffu;
-          if (__builtin_expect(masked, 0))
+          if (__builtin_expect(masked, 0)) {
             vis = visible<NJ>(tok0, sg.len, ctx, row0 + chunk * CN + part + 2 * qd, live_rows, ta.log_group, mask,
                               words);
+            if (post < 0.f) {
+              finish_scores(t_s, SUB, reinterpret_cast<const float*>(ws + pl.ws_rows) + unit * pl.rows + col0,
+                            tm::ldsf(pl.sm_meta + slot * 1024 + 8 * (32 * w + lane)));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) kn[k] = 1.f;
+            }
+          }
           // The running maximum (of score + log2 |v|, so that every weight p |v| stays
           // an fp16 number whatever the norms) moves only when a score passes it by that: in
           // a unit's first tile, afterwards almost never, and all four warps vote together.

@@ -124,9 +124,10 @@ inline bool plan_tree(const Tables& tb, int dtype, int batch, int q_heads, int k
   p->ws_ml = p->slots * p->rows * tb.d * 4;
   p->ws_q = (p->ws_ml + p->slots * p->rows * 8 + 127) / 128 * 128;
   p->ws_scale = p->ws_q + units * p->q_bytes;
+  p->ws_rows = (p->ws_scale + units * 4 + 15) / 16 * 16;
   return true;
 }
 
-inline size_t plan_bytes(const TreePlan& p) { return (size_t)p.ws_scale + (size_t)(p.slots - p.ctas) * 4; }
+inline size_t plan_bytes(const TreePlan& p) { return (size_t)(p.ws_rows + (p.slots - p.ctas) * p.rows * 4); }
 
 }  // namespace tq
