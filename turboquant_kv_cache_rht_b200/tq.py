@@ -235,6 +235,12 @@ class Cache:
                         p(self.v_norm), p(self.k_rnorm), p(self.seq_lens), p(self.status),
                         p(self.append_sync), self.batch, self.kv_heads, self.capacity)
 
+    def tensors(self) -> tuple:
+        """Every array that it has."""
+        ts = (self.k_codes, self.v_codes, self.k_signs, self.k_norm, self.v_norm, self.k_rnorm, self.seq_lens,
+              self.status, self.append_sync)
+        return tuple(t for t in ts if t is not None)
+
     def nbytes(self) -> int:
         ts = [self.k_codes, self.v_codes, self.k_signs, self.k_norm, self.v_norm, self.k_rnorm]
         return sum(t.numel() * t.element_size() for t in ts if t is not None)
@@ -407,11 +413,13 @@ def tq_decode_attention_noalloc(cb: Codebook, cache: Cache, q: torch.Tensor,
 class _on:
     """The device and stream of one call: a context in which the cache's device is
     current and what the call allocates belongs to the stream it runs on; it gives
-    the stream's address.  Nothing is switched where both are current already."""
+    the stream's address.  Nothing is switched where both are current already.  Where
+    the caller names a stream, the call's tensors (and its caches') are marked as used
+    there, so that memory dropped after the call is not handed out again before it."""
 
     __slots__ = ("entered", "index")
 
-    def __init__(self, device: torch.device, stream):
+    def __init__(self, device: torch.device, stream, *used):
         self.entered, self.index = (), device.index
         if stream is None and device.index == torch._C._cuda_getDevice():
             return
@@ -422,6 +430,10 @@ class _on:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
             self.entered.append(torch.cuda.stream(stream))
+            for x in used:
+                for t in x.tensors() if isinstance(x, Cache) else (x,):
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
 
     def __enter__(self) -> int:
         for c in self.entered:
@@ -564,7 +576,7 @@ def tq_rope_append(cb: Codebook, cache: Cache, rope: Rope, k: torch.Tensor, v: t
     pos = _index_ptr(where, "positions", positions, (b, n), dev)
     begin = _index_ptr(where, "start", start, (b,), dev)
     cs = _cache_struct(where, cb, cache, dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream, cache, rope.table, k, v, q, positions, start, q_out, keys_out) as s:
         if q is None:
             q_out = None
         elif q_out is None:
@@ -628,7 +640,7 @@ def tq_tree_attention(cb: Codebook, cache: Cache, q: torch.Tensor, mask: torch.T
         bits = _index_ptr(where, "mask", mask, (n, words) if mask.dim() == 2 else (b, n, words), dev)
         stride = 0 if mask.dim() == 2 else n * words
     cs = _cache_struct(where, cb, cache, dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream, cache, q, mask, out, workspace) as s:
         if out is None:
             out = torch.empty_like(q)
         else:
@@ -661,7 +673,7 @@ def tq_cache_compact(cb: Codebook, cache: Cache, index: torch.Tensor, counts: to
     at = _index_ptr(where, "index", index, (b, h, n) if per_head else (b, n), dev)
     num = _index_ptr(where, "counts", counts, (b,), dev)
     begin = _index_ptr(where, "start", start, (b,), dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream, cache, index, counts, start) as s:
         _check(lib.tq_cache_compact(cb.handle, cs, at, h * n if per_head else n, n if per_head else 0, num, n, begin, s),
                where)
 
@@ -682,7 +694,7 @@ def tq_cache_copy(cb: Codebook, dst: Cache, src: Cache, dst_rows: torch.Tensor, 
     to = _index_ptr(where, "dst_rows", dst_rows, (n,), dev)
     come = _index_ptr(where, "src_rows", src_rows, (n,), dev)
     lens = _index_ptr(where, "lengths", lengths, (n,), dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream, dst, src, dst_rows, src_rows, lengths) as s:
         _check(lib.tq_cache_copy(cb.handle, cd, cs, to, come, lens, n, src.capacity if max_len is None else max_len, s),
                where)
 
