@@ -450,7 +450,7 @@ tq_status tq_cache_compact(const tq_codebook* cb, const tq_cache* cache, const i
  * of row src_rows[i] of src, len_i = lengths[i] (NULL: all) but at most
  * src seq_lens, and its seq_lens becomes len_i; slots from len_i on are left as
  * they were.  dst and src hold the same kv_heads and the same codebook's rows;
- * they may be one cache (rows are forked).
+ * they may be one cache (rows are forked), and otherwise share no memory.
  * dst_rows, src_rows, lengths : DEVICE int32 [n], n at most 65535.
  * max_len : host upper bound of every len_i (it sizes the grid); a longer one is
  *         cut to it and sets TQ_FLAG_MAXCTX.

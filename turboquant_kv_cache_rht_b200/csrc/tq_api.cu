@@ -380,6 +380,21 @@ tq::SlotArrays arrays_of(const tq_codebook* cb, const tq_cache* c) {
   return a;
 }
 
+// Whether two caches share memory without being one cache (the same arrays, rows of the
+// same capacity): a copy could then read what it writes.
+bool overlap(const tq::SlotArrays& a, const tq_cache* ca, const tq::SlotArrays& b, const tq_cache* cb) {
+  bool one = ca->capacity == cb->capacity;
+  for (int i = 0; i < a.n; ++i) one = one && a.p[i] == b.p[i];
+  if (one) return false;
+  auto end = [](const tq::SlotArrays& x, const tq_cache* c, int i) {
+    return (uintptr_t)x.p[i] + (uintptr_t)c->batch * c->kv_heads * c->capacity * x.bytes[i];
+  };
+  for (int i = 0; i < a.n; ++i)
+    for (int j = 0; j < b.n; ++j)
+      if ((uintptr_t)a.p[i] < end(b, cb, j) && (uintptr_t)b.p[j] < end(a, ca, i)) return true;
+  return false;
+}
+
 tq_status cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();
   if (e == cudaErrorNotSupported) return fail(TQ_ERR_UNSUPPORTED, "%s: no kernel for this shape on this device", what);
@@ -689,14 +704,17 @@ tq_status tq_cache_copy(const tq_codebook* cb, const tq_cache* dst, const tq_cac
   if (dst->kv_heads != src->kv_heads)
     return fail(TQ_ERR_INVALID, "kv_heads differ (dst %d, src %d)", dst->kv_heads, src->kv_heads);
   if (dst->kv_heads > 65535) return fail(TQ_ERR_INVALID, "kv_heads %d: at most 65535", dst->kv_heads);
+  const tq::SlotArrays da = arrays_of(cb, dst), sa = arrays_of(cb, src);
+  if (overlap(da, dst, sa, src))
+    return fail(TQ_ERR_INVALID, "dst and src overlap in memory, but are not one cache");
   if (n < 0 || n > 65535) return fail(TQ_ERR_INVALID, "n %d outside [0, 65535]", n);
   if (max_len < 0) return fail(TQ_ERR_INVALID, "max_len %d is negative", max_len);
   if (n == 0) return ok();
   if (!dst_rows || !src_rows) return fail(TQ_ERR_INVALID, "dst_rows or src_rows is NULL");
   if ((uintptr_t)dst_rows % 4 || (uintptr_t)src_rows % 4 || (uintptr_t)lengths % 4)
     return fail(TQ_ERR_INVALID, "dst_rows, src_rows and lengths must be 4-byte aligned");
-  return cuda_status(tq::launch_cache_copy(arrays_of(cb, dst), view_of(dst), arrays_of(cb, src), view_of(src),
-                                           dst_rows, src_rows, lengths, n, max_len, (cudaStream_t)stream),
+  return cuda_status(tq::launch_cache_copy(da, view_of(dst), sa, view_of(src), dst_rows, src_rows, lengths, n, max_len,
+                                           (cudaStream_t)stream),
                      "cache-copy launch");
 }
 
