@@ -139,14 +139,6 @@ __device__ __forceinline__ void ld_32x32b(uint32_t addr, uint32_t (&r)[16]) {
       : TQ_R4(r, 0), TQ_R4(r, 4), TQ_R4(r, 8), TQ_R4(r, 12)
       : "r"(addr));
 }
-__device__ __forceinline__ void st_32x32b(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};" ::"r"(addr),
-      TQ_I4(r, 0), TQ_I4(r, 4), TQ_I4(r, 8), TQ_I4(r, 12), TQ_I4(r, 16), TQ_I4(r, 20), TQ_I4(r, 24), TQ_I4(r, 28)
-      : "memory");
-}
 __device__ __forceinline__ void st_32x32b(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
