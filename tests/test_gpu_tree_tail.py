@@ -41,7 +41,7 @@ def test_a_peak_over_a_flat_tail(codebook, ctx, at, bits):
     q = q.expand(B, n, H, d).contiguous()
     got = tq.tq_tree_attention(cb, cache, q.cuda(), softmax_scale=scale)
     assert torch.equal(got, got[:1, :, :1].expand_as(got))
-    out, tol, acc = bounded_reference(cb, _row(cache), q[:1, :, :1], chain(n), [ctx + n], scale=scale)
+    out, tol, acc = bounded_reference(cb, _row(cache), q[:1, :, :1], chain(n), [ctx + n], scale=scale, share=ctx + n)
     assert_within(got[:1, :, :1], out, tol, acc)
     # a tail that vanished would not pass where it weighs more than the peak's own rounding
     if ctx * 2.0 ** -bits > 2.0 ** -9:

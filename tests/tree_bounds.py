@@ -23,10 +23,11 @@ values v (in the output's frame), output o, rotated query x and keys k:
                  as a 2-norm, which the rotation back keeps
   small weights  a weight below 2^-14 is rounded to a multiple of 2^-24, where the
                  row's largest is at least 2^4: 2^-29 of it per token, at its worst
-  beyond         the above is of first order.  Where a score may be off by more than e =
-                 0.1, the output is still a mean of the values of tokens whose scores are
-                 within 2 e of the largest (others' weights, e^-28 or less, aside): it is
-                 off by no more than the farthest of these values is
+  beyond         the above is of first order.  Where a score may be off by e > 0.1, a
+                 weight is off by a factor of exp(2 e) at most, so the output by (exp(2 e)
+                 - 1) sum_t p_t |v_te - o_e|; and it is still a mean of the values of tokens
+                 whose scores are within 2 e of the largest (others' weights, e^-28 or less,
+                 aside): off by no more than the farthest of these values
 Elements are held to the sum of these, rows to their 2-norm, where the accumulation
 counts once.
 """
@@ -81,9 +82,14 @@ def visible(sees, n, length, end):
     return vis[:, :end]
 
 
-def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
+BLOCKS = 148  # that the tokens of all units are shared out to
+
+
+def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None, drafts=None, share=None):
     """(out, tol, acc) on the cache's device: float64 [B, n, Hq, d] twice, and the
-    accumulation's 2-norm [B, n, Hq, 1]."""
+    accumulation's 2-norm [B, n, Hq, 1].  `drafts`: only these, in this order.  `share`:
+    the most tokens of a row that one block may take (default: a 148th of all rows', and
+    a few tiles)."""
     B, n, Hq, d = q.shape
     H, dev = cache.kv_heads, cache.k_codes.device
     G = Hq // H
@@ -91,9 +97,12 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
     R2 = rotation(cb, True).to(dev) if cb.qjl else None
     scale = 1 / math.sqrt(d) if scale is None else scale
     uq = U if q.dtype == torch.bfloat16 else 2.0 ** -22
-    out = torch.zeros(B, n, Hq, d, dtype=torch.float64, device=dev)
+    drafts = list(range(n)) if drafts is None else drafts
+    if share is None:  # (a unit has at most ceil(rows / 64) blocks of query rows)
+        share = sum(lens) * H * -(-n * G // 64) // BLOCKS + 512
+    out = torch.zeros(B, len(drafts), Hq, d, dtype=torch.float64, device=dev)
     tol = torch.zeros_like(out)
-    acc = torch.zeros(B, n, Hq, 1, dtype=torch.float64, device=dev)
+    acc = torch.zeros(B, len(drafts), Hq, 1, dtype=torch.float64, device=dev)
     q = q.to(dev).double()
     for b in range(B):
         L = lens[b]
@@ -115,10 +124,11 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
                 sign = 2.0 * _codes(cache.k_signs[b, h, :end], 1).double() - 1.0
                 rn = torch.where(used[:, 0], cache.k_rnorm[b, h, :end].double(), zero) * math.sqrt(math.pi / (2 * d))
             unit = q[b, :, h * G:(h + 1) * G]
-            # below 2^-14 a query's half step is 2^-25, where |sqrt(d) x| <= d max|q| is brought to
-            # 2^14 (2^10), by the unit's largest row or, where rows differ by 2^16, by its own
-            tiny = math.sqrt(d) * 2.0 ** ((11 if not cb.qjl else 15) - 36)
-            for i in range(n):
+            # below 2^-14 a query's half step is 2^-25, where d max|q| (which bounds sqrt(d) |x|) is
+            # brought to 2^13 .. 2^14 (2^9 .. 2^10 with the sketch), that of the unit's largest row
+            # or, where rows differ by more than 2^16, of its own: 2^-25 2^-13 sqrt(d) max|q| of x
+            tiny = math.sqrt(d) * 2.0 ** (-34 if cb.qjl else -38)
+            for at, i in enumerate(drafts):
                 for g in range(G):
                     x = R1 @ unit[i, g]
                     floor = torch.minimum(unit.abs().max(), 2.0 ** 17 * unit[i, g].abs().max()) * tiny
@@ -134,7 +144,7 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
 
                     s, p = weights(k)
                     o = p @ v
-                    out[b, i, h * G + g] = o
+                    out[b, at, h * G + g] = o
                     o_table = weights(kt)[1] @ vt
                     away = v - o
                     xx = (x * x + floor * floor * (2.0 ** 22 if uq == U else 2.0 ** 44))
@@ -161,11 +171,13 @@ def bounded_reference(cb, cache, q, sees, lens, scale=None, max_ctx=None):
                     t = t + first * (1 + 2 * worst) + (p * lin) @ away.abs()
                     e = worst + lin[vis[i]].max() if any_seen else zero
                     if float(e) > 0.1:
-                        t = t + away[s >= s.max() - 2 * e - 28].abs().amax(0)
-                    acc[b, i, h * G + g] = (end / 16 + 64) * 2.0 ** -23 * (p @ stored.abs()).norm()
+                        far = away[s >= s.max() - 2 * e - 28].abs().amax(0)
+                        # (past e = 10 the smaller weights are not held exactly enough for the first)
+                        t = t + (far if float(e) > 10 else torch.minimum(far, torch.expm1(2 * e) * (p @ away.abs())))
+                    acc[b, at, h * G + g] = (min(end, share) / 16 + 64) * 2.0 ** -23 * (p @ stored.abs()).norm()
                     small = (p * vn).max() * 2.0 ** -29
                     t = t + small * (v.abs() / vn.clamp_min(1e-300)[:, None]).masked_fill(~vis[i][:, None], 0.0).sum(0)
-                    tol[b, i, h * G + g] = t + (o_table - o).abs()
+                    tol[b, at, h * G + g] = t + (o_table - o).abs()
     return out, tol, acc
 
 
@@ -191,3 +203,8 @@ def passes(wrong, out, tol, acc, dtype):
     """Whether a wrong answer would pass for the right one in some row that it changes."""
     worst = _worst((wrong.to(dtype).double() - out).abs(), out, tol, acc, dtype)
     return bool((worst <= 1)[(wrong != out).any(-1)].any())
+
+
+def found(wrong, out, tol, acc, dtype):
+    """Whether assert_within would refuse a wrong answer: some row of it is out of bounds."""
+    return bool((_worst((wrong.to(dtype).double() - out).abs(), out, tol, acc, dtype) > 1).any())
