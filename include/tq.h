@@ -389,7 +389,7 @@ typedef struct {
  *         skipped and sets TQ_FLAG_INDEX.
  * Then seq_lens[b] = start + n_new.  A row that would pass `capacity` is skipped
  * and sets TQ_FLAG_CAPACITY.  The queries (and k_out) of a skipped row are
- * written all the same.  Outputs must not overlap inputs.  append_sync is used
+ * written all the same.  Outputs that overlap inputs, or one another, are refused.  append_sync is used
  * as by tq_quantize_append.  n_new == 0 is a no-op. */
 tq_status tq_rope_append(const tq_codebook* cb, const tq_cache* cache, const tq_rope* rope,
                          const tq_heads* q, int q_heads, const tq_heads* k, const tq_heads* v,

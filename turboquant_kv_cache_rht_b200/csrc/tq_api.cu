@@ -655,6 +655,25 @@ tq_status tq_rope_append(const tq_codebook* cb, const tq_cache* cache, const tq_
     return fail(TQ_ERR_INVALID, "q_out and k_out must be 16-byte aligned");
   if ((uintptr_t)positions % 4 || (uintptr_t)start % 4)
     return fail(TQ_ERR_INVALID, "positions and start must be 4-byte aligned");
+  // blocks read one token's heads while others write: no output may lie where an input does
+  struct Range {
+    uintptr_t lo, hi;
+    bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
+  };
+  auto dense = [&](const void* p, int heads) {
+    const uintptr_t at = (uintptr_t)p;
+    return Range{at, p ? at + (uintptr_t)esz * cache->batch * n_new * heads * d : at};
+  };
+  const int counts[] = {cache->kv_heads, cache->kv_heads, q ? q_heads : 0};
+  const Range outs[] = {dense(q ? q_out : nullptr, counts[2]), dense(k_out, counts[0])};
+  for (int i = 0; i < (q ? 3 : 2); ++i) {
+    const tq_heads& h = *views[i];
+    const uintptr_t last = (uintptr_t)(h.stride_b * (cache->batch - 1) + h.stride_h * (counts[i] - 1) +
+                                       h.stride_t * (int64_t)(n_new - 1) + d);
+    const Range in{(uintptr_t)h.data, (uintptr_t)h.data + (uintptr_t)esz * last};
+    if (in.meets(outs[0]) || in.meets(outs[1])) return fail(TQ_ERR_INVALID, "q_out or k_out overlaps %s", names[i]);
+  }
+  if (outs[0].meets(outs[1])) return fail(TQ_ERR_INVALID, "q_out and k_out overlap");
   tq::RopeAppend ra;
   ra.table = rope->table;
   ra.max_pos = rope->max_pos;
