@@ -524,8 +524,9 @@ def prepare(case, seed):
 
 
 def _handle(tq, cb, cache, rows, kv_heads, capacity):
-    """The framework's cache over these tensors."""
-    handle = tq.Cache(cb, rows, kv_heads, capacity)
+    """The framework's cache over these tensors (its own are a few slots, and replaced)."""
+    handle = tq.Cache(cb, rows, kv_heads, 16)
+    handle.capacity = capacity
     for name, tensor in cache.items():
         setattr(handle, name, tensor)
     return handle
