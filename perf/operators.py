@@ -517,6 +517,8 @@ def prepare(case, seed):
             s["rope"] = tq.Rope(case["rot_dim"], s["positions"], base=ROPE_BASE, interleaved=case["interleaved"],
                                 scaling=None if case["scaling"] == "none" else case["scaling"], factor=ROPE_FACTOR,
                                 original_max=ROPE_ORIGINAL)
+        if case["op"] == "compact":
+            s["full"] = s["cache"]["seq_lens"].clone()
         if case["op"] == "copy":
             s["to_handle"] = s["handle"] if case["fork"] else _handle(tq, s["cb"], s["to"], rows, case["kv_heads"],
                                                                       capacity)
@@ -614,6 +616,7 @@ def _run_append(s):
 def _run_compact(s):
     c, cache = s["case"], s["cache"]
     if own:
+        cache["seq_lens"].copy_(s["full"])  # a pass before this one has left the kept slots' lengths
         s["tq"].tq_cache_compact(s["cb"], s["handle"], s["index"], s["counts"], start=s["start"])
         return dict(cache)
     b, h = c["batch"], c["kv_heads"]
