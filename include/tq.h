@@ -389,8 +389,9 @@ typedef struct {
  *         skipped and sets TQ_FLAG_INDEX.
  * Then seq_lens[b] = start + n_new.  A row that would pass `capacity` is skipped
  * and sets TQ_FLAG_CAPACITY.  The queries (and k_out) of a skipped row are
- * written all the same.  Outputs that overlap inputs, or one another, are refused.  append_sync is used
- * as by tq_quantize_append.  n_new == 0 is a no-op. */
+ * written all the same.  Outputs that overlap inputs, or one another, are
+ * refused.  append_sync is used as by tq_quantize_append.  n_new == 0 is a
+ * no-op. */
 tq_status tq_rope_append(const tq_codebook* cb, const tq_cache* cache, const tq_rope* rope,
                          const tq_heads* q, int q_heads, const tq_heads* k, const tq_heads* v,
                          tq_dtype dtype, int n_new, const int32_t* positions, int relative,
@@ -413,16 +414,18 @@ size_t tq_tree_workspace_bytes(const tq_codebook* cb, int batch, int q_heads, in
  * out  : DEVICE `dtype`, like q.
  * The products' operands are fp16, their sums, the scores, maxima and sums fp32: the
  * weights are rounded to fp16 (one below 2^-29 of a row's largest may be lost, so 128k
- * such tokens cost 2^-12 of the row at most), and so are the rotated queries of a bf16 call (an
- * fp16 call holds them in two parts, 22 bits) and the affine codec's keys and values.
- * Queries of one call may differ in size by any factor; a query that is not finite
- * makes its own row NaN.  A draft that attends nothing gives zeros, as do all drafts of a row that holds
- * fewer than n_q tokens.  What a draft does not attend never reaches it, whatever
- * the cache holds there; a token whose value has no finite norm (or scale, or bias)
- * makes the drafts that attend it NaN.  softmax_scale, max_ctx, workspace: as for
- * tq_decode_attention (tokens at max_ctx and past it, drafts among them, are not
- * attended and set TQ_FLAG_MAXCTX).  q_heads / kv_heads is 1, 2, 4 or 8 and the
- * code widths are those of the decode.  The result is deterministic. */
+ * such tokens cost 2^-12 of the row at most), and so are the rotated queries of a bf16
+ * call (an fp16 call holds them in two parts, 22 bits), the sketch's queries and factor,
+ * and the affine codec's keys and values.
+ * Queries of one call may differ in size by any factor (a score past fp32's range is
+ * infinite); a query that is not finite makes its own row NaN.  A draft that attends
+ * nothing gives zeros, as do all drafts of a row that holds fewer than n_q tokens.  What
+ * a draft does not attend never reaches it, whatever the cache holds there; a token
+ * whose value has no finite norm (or scale, or bias) makes the drafts that attend it
+ * NaN.  softmax_scale, max_ctx, workspace: as for tq_decode_attention (tokens at max_ctx
+ * and past it, drafts among them, are not attended and set TQ_FLAG_MAXCTX).  q_heads /
+ * kv_heads is 1, 2, 4 or 8 and the code widths are those of the decode.  The result is
+ * deterministic. */
 tq_status tq_tree_attention(const tq_codebook* cb, const tq_cache* cache, const void* q,
                             tq_dtype dtype, int q_heads, int n_q, const uint32_t* mask,
                             int64_t mask_stride, float softmax_scale, int max_ctx, void* out,
